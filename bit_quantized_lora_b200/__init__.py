@@ -34,6 +34,9 @@ __all__ = [
     "ft_quantize", "ft_quantize_transpose", "ft_linear_fwd", "ft_linear_bwd",
     "ft_workspace_bytes", "ft_quantize_workspace_bytes", "ft_device_error",
     "ft_set_cooperative_quantizer", "ft_set_gemm_mode", "GEMM_PAIRS", "GEMM_SINGLE", "prepare_layer", "svd_split", "Workspace", "timing",
+    "GatedNorm", "GatedNormGrads", "NORM_NONE", "NORM_RMS", "NORM_LAYER", "ft_gated_norm_fwd", "ft_gated_norm_bwd",
+    "ft_gelu_bwd_bf16", "Rope", "ROPE_PAIRS", "ROPE_HALVES", "rope_freqs", "ft_qk_rope_fwd", "ft_qk_rope_bwd",
+    "AdamW", "ft_adamw_decode",
 ]
 
 
@@ -410,3 +413,9 @@ class timing:
         n = ctypes.c_int64(0)
         check("ft_timing_read", load().ft_timing_read(kernel.encode(), ctypes.byref(ms), ctypes.byref(n)))
         return ms.value, n.value
+
+
+from .blockops import (NORM_LAYER, NORM_NONE, NORM_RMS, ROPE_HALVES, ROPE_PAIRS, GatedNorm,  # noqa: E402
+                       GatedNormGrads, Rope, ft_gated_norm_bwd, ft_gated_norm_fwd, ft_gelu_bwd_bf16,
+                       ft_qk_rope_bwd, ft_qk_rope_fwd, rope_freqs)
+from .optim import AdamW, ft_adamw_decode  # noqa: E402

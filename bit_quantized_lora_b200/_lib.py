@@ -43,6 +43,101 @@ class FtLinear(ctypes.Structure):
     ]
 
 
+class FtGatedNorm(ctypes.Structure):
+    _fields_ = [
+        ("M", c_i64),
+        ("D", c_i64),
+        ("B", c_i64),
+        ("offsets", c_vp),
+        ("pre", ctypes.c_int32),
+        ("post", ctypes.c_int32),
+        ("eps_pre", ctypes.c_float),
+        ("eps_post", ctypes.c_float),
+        ("alpha", ctypes.c_float),
+        ("xt", ctypes.c_int32),
+        ("pt", ctypes.c_int32),
+        ("ld_gate", c_i64),
+        ("ld_scale", c_i64),
+        ("ld_shift", c_i64),
+        ("gate", c_vp),
+        ("scale", c_vp),
+        ("shift", c_vp),
+        ("w_post", c_vp),
+        ("w", c_vp),
+        ("bias", c_vp),
+    ]
+
+
+class FtGatedNormGrads(ctypes.Structure):
+    _fields_ = [
+        ("dx", c_vp),
+        ("lddx", c_i64),
+        ("dy", c_vp),
+        ("lddy", c_i64),
+        ("dgate", c_vp),
+        ("dscale", c_vp),
+        ("dshift", c_vp),
+        ("dw_post", c_vp),
+        ("dw", c_vp),
+        ("dbias", c_vp),
+        ("amax_dy", c_vp),
+    ]
+
+
+class FtRope(ctypes.Structure):
+    _fields_ = [
+        ("M", c_i64),
+        ("S", c_i64),
+        ("Hq", ctypes.c_int32),
+        ("Hk", ctypes.c_int32),
+        ("hd", ctypes.c_int32),
+        ("n_axes", ctypes.c_int32),
+        ("axis_dims", ctypes.c_int32 * 4),
+        ("layout", ctypes.c_int32),
+        ("norm", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("post", ctypes.c_int32),
+        ("pt", ctypes.c_int32),
+        ("pos", c_vp),
+        ("freqs", c_vp),
+        ("w_q", c_vp),
+        ("w_k", c_vp),
+    ]
+
+
+class FtHeads(ctypes.Structure):
+    _fields_ = [
+        ("p", c_vp),
+        ("sb", c_i64),
+        ("sh", c_i64),
+        ("st", c_i64),
+    ]
+
+
+class FtAdamwTensor(ctypes.Structure):
+    _fields_ = [
+        ("p", c_vp),
+        ("p16", c_vp),
+        ("grad", c_vp),
+        ("m", c_vp),
+        ("v", c_vp),
+        ("m_scale", c_vp),
+        ("v_scale", c_vp),
+        ("n", c_i64),
+        ("weight_decay", ctypes.c_float),
+        ("gt", ctypes.c_int32),
+    ]
+
+
+class FtAdamwHyper(ctypes.Structure):
+    _fields_ = [
+        ("lr", ctypes.c_double),
+        ("beta1", ctypes.c_double),
+        ("beta2", ctypes.c_double),
+        ("eps", ctypes.c_double),
+    ]
+
+
 # name -> (restype, argtypes), exactly the declarations of include/ft.h
 SIGNATURES = {
     "ft_quantize": (ctypes.c_int, [c_vp, c_i64, c_i64, c_i64, ctypes.c_int, c_vp,
@@ -75,6 +170,21 @@ SIGNATURES = {
     "ft_linear_fwd_noalloc": (ctypes.c_int, [ctypes.POINTER(FtLinear), c_vp, c_i64, c_vp, c_vp,
                                              ctypes.c_int, c_vp, c_vp]),
     "ft_linear_fwd_noalloc_max_bytes": (ctypes.c_size_t, []),
+    "ft_gated_norm_fwd": (ctypes.c_int, [ctypes.POINTER(FtGatedNorm), c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp,
+                                         c_i64, c_vp, c_vp, c_vp]),
+    "ft_gated_norm_bwd": (ctypes.c_int, [ctypes.POINTER(FtGatedNorm), c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp,
+                                         c_i64, c_vp, ctypes.POINTER(FtGatedNormGrads), c_vp, ctypes.c_size_t, c_vp]),
+    "ft_gated_norm_workspace_bytes": (ctypes.c_size_t, [c_i64, c_i64, c_i64]),
+    "ft_gelu_bwd_bf16": (ctypes.c_int, [c_vp, c_vp, c_vp, c_i64, c_vp, c_vp]),
+    "ft_qk_rope_fwd": (ctypes.c_int, [ctypes.POINTER(FtRope), c_vp, c_i64, ctypes.POINTER(FtHeads),
+                                      ctypes.POINTER(FtHeads), ctypes.POINTER(FtHeads), c_vp]),
+    "ft_qk_rope_bwd": (ctypes.c_int, [ctypes.POINTER(FtRope), ctypes.POINTER(FtHeads), ctypes.POINTER(FtHeads),
+                                      ctypes.POINTER(FtHeads), c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_vp, c_vp,
+                                      ctypes.c_size_t, c_vp]),
+    "ft_qk_rope_workspace_bytes": (ctypes.c_size_t, [c_i64, c_i64]),
+    "ft_adamw_step": (ctypes.c_int, [c_vp, c_i64, ctypes.POINTER(FtAdamwHyper), ctypes.c_int, c_vp, c_vp, c_vp,
+                                     c_vp]),
+    "ft_adamw_decode": (ctypes.c_int, [c_vp, c_vp, c_i64, ctypes.c_int, c_vp, c_vp]),
     "ft_timing_enable": (ctypes.c_int, [ctypes.c_int]),
     "ft_timing_read": (ctypes.c_int, [ctypes.c_char_p, ctypes.POINTER(ctypes.c_double),
                                       ctypes.POINTER(c_i64)]),

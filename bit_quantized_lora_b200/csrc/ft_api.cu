@@ -9,6 +9,7 @@
 #include <algorithm>
 #include <atomic>
 #include <chrono>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -17,11 +18,15 @@
 #include "../../include/ft.h"
 #include "ft_nvfp4.cuh"
 #include "ft_ptx.cuh"
+#include "k_adamw.cuh"
+#include "k_gelu_bwd.cuh"
 #include "k_gemm_fp4.cuh"
 #include "k_lora_grad.cuh"
+#include "k_norm.cuh"
 #include "k_qdown.cuh"
 #include "k_qres.cuh"
 #include "k_quant.cuh"
+#include "k_rope.cuh"
 
 namespace {
 
@@ -224,12 +229,22 @@ enum KernelId {
     KID_GEMM_BF16,
     KID_DEQUANT_W,
     KID_GELU,
+    KID_NORM_FWD,
+    KID_NORM_BWD,
+    KID_NORM_REDUCE,
+    KID_GELU_BWD,
+    KID_ROPE_FWD,
+    KID_ROPE_BWD,
+    KID_ROPE_REDUCE,
+    KID_ADAMW,
+    KID_ADAMW_DECODE,
     KID_COUNT
 };
 const char* const kKernelNames[KID_COUNT] = {
     "k_amax_bf16", "k_quant_1x16", "k_quant_tile16", "k_pack_lt", "k_qdown",
     "k_lowrank_finalize", "k_gemm_fp4", "k_lora_grad", "k_lora_grad_reduce", "k_qres",
-    "k_gemm_bf16", "k_dequant_w", "k_gelu_bf16"};
+    "k_gemm_bf16", "k_dequant_w", "k_gelu_bf16", "k_gated_norm_fwd", "k_gated_norm_bwd", "k_gated_norm_reduce",
+    "k_gelu_bwd_bf16", "k_qk_rope_fwd", "k_qk_rope_bwd", "k_qk_rope_reduce", "k_adamw", "k_adamw_decode"};
 
 struct TimingRec {
     cudaEvent_t a, b;
@@ -1405,3 +1420,5 @@ extern "C" ft_status ft_linear_fwd_noalloc(const ft_linear* L, const void* X, in
 }
 
 extern "C" size_t ft_linear_fwd_noalloc_max_bytes(void) { return kNoAllocScratchBytes; }
+
+#include "ft_block_api.cuh"

@@ -385,6 +385,232 @@ ft_status ft_linear_fwd_noalloc(const ft_linear* L, const void* X, int64_t M, co
                                 void* Y, ft_dtype yt, void* P_save, void* stream);
 size_t ft_linear_fwd_noalloc_max_bytes(void);
 
+/* ======================================================================
+ * Operators of a DiT block around its linears: the norms with their gate,
+ * residual and modulation, the rotary positions of queries and keys, the
+ * backward of GELU, and the optimizer step of the adapters.  They hand the
+ * linears the tensor amax of what they write (amax_h, amax_dy, amax: raised
+ * to the largest stored magnitude like ft_linear_fwd's amax_y), so that
+ * ft_linear_fwd / ft_linear_bwd quantize in a single pass.
+ *
+ * Beyond the conventions above:
+ *   - They keep no state between calls and use no epochs: a call may be
+ *     captured in a CUDA graph and replayed.  A workspace serves one call at
+ *     a time (calls that may run at the same time take one each, graphs
+ *     among them); it needs no clearing.
+ *   - An output may be the very buffer of an input of the same type, shape
+ *     and leading dimension (in place); buffers that overlap otherwise are
+ *     outside the contract.
+ *   - NaN and Inf propagate to what is computed from them as in the
+ *     formulas; an amax ignores NaN.
+ *   - Sums, statistics and everything between loads and stores are FP32;
+ *     each stored value is rounded once, to nearest even.
+ *   - Results do not change from run to run.
+ * ====================================================================== */
+
+typedef enum { FT_NORM_NONE = 0, FT_NORM_RMS = 1, FT_NORM_LAYER = 2 } ft_norm_kind;
+
+/* A block's boundary: the gated residual of the sub-block before it and the
+ * modulated norm of the sub-block behind it.  For row i of sample b:
+ *     u = y_i, or N_post(y_i) * w_post
+ *     r = x_i + alpha * gate_b * u                    stored as xt
+ *     h = (N_pre(r) * w + bias) * (1 + scale_b) + shift_b       r as stored
+ *   N is RMS norm x / sqrt(mean(x^2) + eps) or layer norm
+ *   (x - mean) / sqrt(mean((x - mean)^2) + eps) over the D channels.
+ *   M rows of D channels; D a multiple of 8, at most 8192; M at most 2^30.
+ *   B samples.  offsets: device int32 [B + 1], ascending from 0; rows
+ *     offsets[b] .. offsets[b+1] - 1 are sample b's (none, one or many);
+ *     rows from offsets[B] on are left as they were, in every output.  Or
+ *     NULL: M / B rows each (M a multiple of B).
+ *   xt: type of the residual stream x, r, dr, dx.  y, h, dh, dy are bf16.
+ *   pt: type of gate, scale, shift [B, D] (ld_gate, ld_scale, ld_shift
+ *     elements from sample to sample, 0 = one for all), w_post, w, bias [D].
+ *     Any may be NULL (gate: 1, scale and shift: 0, w_post and w: 1, bias:
+ *     0).  gate and w_post need y; w_post needs post; scale, shift, w, bias
+ *     need pre.                                                            */
+typedef struct {
+    int64_t M, D, B;
+    const int32_t* offsets;
+    int32_t pre, post; /* ft_norm_kind */
+    float eps_pre, eps_post, alpha;
+    int32_t xt, pt; /* ft_dtype */
+    int64_t ld_gate, ld_scale, ld_shift;
+    const void *gate, *scale, *shift;
+    const void *w_post, *w, *bias;
+} ft_gated_norm;
+
+/* ft_gated_norm_fwd -- r, h and the rows' statistics.
+ *   y     : bf16 [M, D], or NULL: no residual (r = x, not written; post and
+ *           gate must be absent).
+ *   r     : [M, D] of type xt, out (NULL without y).  May be x.
+ *   h     : bf16 [M, D], out; NULL exactly when pre is FT_NORM_NONE.
+ *   stats : NULL, or FP32 [M, 4] out: mean and 1/deviation of r, then of y
+ *           (0 and 1 for a norm that is absent, 0 for the mean of an RMS
+ *           norm); 16-byte aligned.  The backward reads it.
+ *   amax_h: NULL, or a device float >= 0 raised to max|h|.                 */
+ft_status ft_gated_norm_fwd(const ft_gated_norm* n, const void* x, int64_t ldx, const void* y, int64_t ldy, void* r,
+                            int64_t ldr, void* h, int64_t ldh, float* stats, float* amax_h, void* stream);
+
+/* Gradients that ft_gated_norm_bwd writes.
+ *   dx  : [M, D] of type xt (NULL: not wanted), the gradient of x:
+ *         d = dr + the gradient through N_pre.   May be dr.
+ *   dy  : bf16 [M, D] (NULL: not wanted), the gradient of y:
+ *         alpha * gate * d (times w_post and through N_post).
+ *   dgate, dscale, dshift: FP32 [B, D] dense, and dw_post, dw, dbias: FP32
+ *         [D]; each NULL or overwritten.  An empty sample's are zero.  They
+ *         need what they are the gradient of to be present, dshift and dbias
+ *         excepted (which need pre).
+ *   amax_dy: NULL, or a device float >= 0 raised to max|dy|.               */
+typedef struct {
+    void* dx;
+    int64_t lddx;
+    void* dy;
+    int64_t lddy;
+    float *dgate, *dscale, *dshift;
+    float *dw_post, *dw, *dbias;
+    float* amax_dy;
+} ft_gated_norm_grads;
+
+/* ft_gated_norm_bwd -- the gradients of the above.
+ *   dh : bf16 [M, D], the gradient of h (NULL when pre is FT_NORM_NONE).
+ *   dr : [M, D] of type xt, the gradient of r from the blocks above, or
+ *        NULL (zero).  One of dh, dr is given.
+ *   r  : the forward's r (x where there was no y); NULL when pre is absent.
+ *   y  : the forward's y; needed with post or dgate.
+ *   stats: the forward's (NULL when neither norm is present).
+ *   ws : ft_gated_norm_workspace_bytes(M, D, B) bytes where any of dgate ..
+ *        dbias is wanted.                                                  */
+ft_status ft_gated_norm_bwd(const ft_gated_norm* n, const void* dh, int64_t lddh, const void* dr, int64_t lddr,
+                            const void* r, int64_t ldr, const void* y, int64_t ldy, const float* stats,
+                            const ft_gated_norm_grads* g, void* ws, size_t ws_bytes, void* stream);
+size_t ft_gated_norm_workspace_bytes(int64_t M, int64_t D, int64_t B);
+
+/* ft_gelu_bwd_bf16 -- dy = dh * GELU'(y), GELU'(y) = Phi(y) + y phi(y): the
+ * backward of ft_gelu_bf16, for the MLP's own backward.
+ *   y, dh, dy: bf16 [n], 16-byte aligned; n a multiple of 8; dy may be dh or y.
+ *   amax_dy: NULL, or a device float >= 0 raised to max|dy|.               */
+ft_status ft_gelu_bwd_bf16(const void* y, const void* dh, void* dy, int64_t n, float* amax_dy, void* stream);
+
+/* Types of positions. */
+typedef enum { FT_POS_I32 = 0, FT_POS_F32 = 1 } ft_pos_dtype;
+/* Which values of a head form a pair: (2j, 2j + 1), or (j, j + rot / 2). */
+typedef enum { FT_ROPE_PAIRS = 0, FT_ROPE_HALVES = 1 } ft_rope_layout;
+
+/* Rotary positions with several axes (time, height, width) on the queries
+ * and keys of a QKV linear's output, with an optional RMS norm of each head
+ * before it.  Row m of qkv holds Hq query heads, Hk key heads and Hk value
+ * heads of hd values.  The first rot values of a query or key head form
+ * rot / 2 pairs; pair j turns by the angle pos[m, a(j)] * freqs[j], where
+ * axis a owns the next axis_dims[a] / 2 pairs; the rest pass through:
+ *     (p, q) -> (p cos - q sin, q cos + p sin)
+ *   Angles are formed and reduced in FP64 (a far position keeps its turn).
+ *   hd: a multiple of 8, at most 256; rot = the sum of axis_dims (each even)
+ *     <= hd; for FT_ROPE_HALVES a multiple of 8.  n_axes: 1 to 4.
+ *   S : rows per sample of the outputs' layout (row m = token m % S of sample
+ *     m / S); M a multiple of S.
+ *   pos  : [M, n_axes] dense, of type post.
+ *   freqs: device FP64 [rot / 2], radians per position.
+ *   norm : FT_NORM_NONE or FT_NORM_RMS (eps); w_q, w_k: its weights [hd], of
+ *     type pt, or NULL (1).                                                */
+typedef struct {
+    int64_t M, S;
+    int32_t Hq, Hk, hd, n_axes;
+    int32_t axis_dims[4];
+    int32_t layout; /* ft_rope_layout */
+    int32_t norm;   /* ft_norm_kind */
+    float eps;
+    int32_t post; /* ft_pos_dtype */
+    int32_t pt;   /* ft_dtype */
+    const void* pos;
+    const double* freqs;
+    const void *w_q, *w_k;
+} ft_rope;
+
+/* Heads of an attention operand, bf16: head h of token s of sample b starts
+ * at p + b * sb + h * sh + s * st (elements; multiples of 8), its values are
+ * contiguous.                                                              */
+typedef struct {
+    void* p;
+    int64_t sb, sh, st;
+} ft_heads;
+
+/* ft_qk_rope_fwd -- splits qkv (bf16 [M, (Hq + 2 Hk) hd], leading dimension
+ * ld) into q, k (normed and rotated) and v (as it is; v->p NULL: not copied).
+ * q, k, v may be the parts of qkv themselves (in place).                   */
+ft_status ft_qk_rope_fwd(const ft_rope* R, const void* qkv, int64_t ld, const ft_heads* q, const ft_heads* k,
+                         const ft_heads* v, void* stream);
+
+/* ft_qk_rope_bwd -- the gradient of qkv from those of q, k and v.
+ *   qkv : the forward's input; needed with a norm (NULL otherwise).
+ *   dqkv: bf16 [M, (Hq + 2 Hk) hd], out.  dv->p NULL: its value columns are
+ *         left as they were.
+ *   dw_q, dw_k: FP32 [hd] out, or NULL; they need the norm.
+ *   amax: NULL, or a device float >= 0 raised to max|dqkv| over the columns
+ *         written.
+ *   ws  : ft_qk_rope_workspace_bytes(M, hd) bytes where dw_q or dw_k is wanted. */
+ft_status ft_qk_rope_bwd(const ft_rope* R, const ft_heads* dq, const ft_heads* dk, const ft_heads* dv,
+                         const void* qkv, int64_t ld, void* dqkv, int64_t lddqkv, float* dw_q, float* dw_k,
+                         float* amax, void* ws, size_t ws_bytes, void* stream);
+size_t ft_qk_rope_workspace_bytes(int64_t M, int64_t hd);
+
+/* One parameter tensor of an AdamW step, n elements.
+ *   p   : FP32 master weights, updated; or NULL.
+ *   p16 : bf16 weights; or NULL.  With p they receive its rounded copy,
+ *         without it they are updated themselves.  One of the two is given.
+ *   grad: of type gt.
+ *   m, v: the moments: FP32, or with 8-bit states int8 codes (m) and uint8
+ *         codes (v), with one FP32 scale per 256 consecutive elements
+ *         (m_scale, v_scale [ceil(n / 256)]; NULL with 32-bit states).
+ *   weight_decay: this tensor's.
+ * Pointers are aligned to their element type; tensors whose pointers are
+ * 16-byte aligned (8-byte for codes) take the vector path.                 */
+typedef struct {
+    float* p;
+    void* p16;
+    const void* grad;
+    void* m;
+    void* v;
+    float* m_scale;
+    float* v_scale;
+    int64_t n;
+    float weight_decay;
+    int32_t gt; /* ft_dtype */
+} ft_adamw_tensor;
+
+/* ft_adamw_step -- one AdamW step (decoupled weight decay) of all tensors,
+ * t = *step + 1:
+ *     m = beta1 m + (1 - beta1) g        v = beta2 v + (1 - beta2) g^2
+ *     p = p (1 - lr wd) - lr / (1 - beta1^t) * m / (sqrt(v / (1 - beta2^t)) + eps)
+ * with g = grad * (*grad_scale).  The moments of the update are the fresh
+ * FP32 ones; with 8-bit states they are then stored as codes, per block of
+ * 256 with top = the block's largest |m| (v), each step rounded to nearest
+ * in IEEE FP32:
+ *     m: sign * c, c = rint(127 sqrt(|m| (1 / top)));       m' = (c|c| / 127^2) top
+ *     v: c = rint(255 sqrt(sqrt(v (1 / top))));             v' = (c^2 / 255^2)^2 top
+ * (all codes 0 where top < 2^-126).  The powers spread the codes: m keeps
+ * 1 / 127^2 and v 1 / 255^4 of their block's largest.  A non-finite moment
+ * makes its block's scale NaN.
+ *   t        : host array of `count` tensors; read during the call only.
+ *   state_bits: 32 or 8.
+ *   step     : device int64 [2], zero before the first step: the number of
+ *              steps done, which the call raises by one, and a word of its
+ *              own.  It is the optimizer's and serves one call at a time.
+ *   lr_dev   : NULL, or a device float used in place of lr (a captured step
+ *              whose rate changes).
+ *   grad_scale: NULL, or a device float (1 / ranks, a clipping factor).
+ * Tensors with n = 0 are skipped; the step still counts.                   */
+typedef struct {
+    double lr, beta1, beta2, eps;
+} ft_adamw_hyper;
+ft_status ft_adamw_step(const ft_adamw_tensor* t, int64_t count, const ft_adamw_hyper* h, int state_bits,
+                        int64_t* step, const float* lr_dev, const float* grad_scale, void* stream);
+
+/* ft_adamw_decode -- the FP32 values that 8-bit states stand for (to look at
+ * them, to save them, to go on with 32-bit states).
+ *   codes: n codes; scales [ceil(n / 256)]; second: 0 = first moments
+ *   (int8), 1 = second moments (uint8); out: FP32 [n].                     */
+ft_status ft_adamw_decode(const void* codes, const float* scales, int64_t n, int second, float* out, void* stream);
+
 /* Measurement support (no counterpart in the method; used to report each
  * kernel's roofline fraction from inside a real step).  While enabled, every
  * kernel launch of the library is bracketed by two CUDA events on its
