@@ -232,6 +232,7 @@ enum KernelId {
     KID_NORM_FWD,
     KID_NORM_BWD,
     KID_NORM_REDUCE,
+    KID_NORM_WEIGHTS,
     KID_GELU_BWD,
     KID_ROPE_FWD,
     KID_ROPE_BWD,
@@ -244,7 +245,7 @@ const char* const kKernelNames[KID_COUNT] = {
     "k_amax_bf16", "k_quant_1x16", "k_quant_tile16", "k_pack_lt", "k_qdown",
     "k_lowrank_finalize", "k_gemm_fp4", "k_lora_grad", "k_lora_grad_reduce", "k_qres",
     "k_gemm_bf16", "k_dequant_w", "k_gelu_bf16", "k_gated_norm_fwd", "k_gated_norm_bwd", "k_gated_norm_reduce",
-    "k_gelu_bwd_bf16", "k_qk_rope_fwd", "k_qk_rope_bwd", "k_qk_rope_reduce", "k_adamw", "k_adamw_decode"};
+    "k_gated_norm_weights", "k_gelu_bwd_bf16", "k_qk_rope_fwd", "k_qk_rope_bwd", "k_qk_rope_reduce", "k_adamw", "k_adamw_decode"};
 
 struct TimingRec {
     cudaEvent_t a, b;

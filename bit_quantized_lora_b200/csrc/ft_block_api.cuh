@@ -16,37 +16,47 @@ inline bool rows_al16(const void* p, int64_t ld, int elem) { return al16(p) && (
 
 // ------------------------------------------------------------ gated norm
 // Threads of a row: below 33 vectors of eight a power of two of lanes, with
-// several rows per block; above, the block, with one vector per thread up to
-// 512 and two beyond (three sums per column live in registers backward).
+// several rows per block; above, a block of its own with `v` vectors per
+// thread.
 struct RowShape {
     bool wide;
     int v, tpr, threads;
 };
-RowShape row_shape(int64_t D) {
+RowShape row_shape(int64_t D, bool backward) {
     const int nvec = (int)(D / 8);
     if (nvec <= 32) {
         int t = 8;
         while (t < nvec) t *= 2;
         return {false, 1, t, 256};
     }
-    const int v = nvec > 512 ? 2 : 1;
+    const int v = backward ? (nvec > 512 ? 2 : 1) : nvec <= 128 ? 1 : nvec <= 256 ? 2 : 4;
     const int t = (cdiv(nvec, v) + 31) / 32 * 32;
     return {true, v, t, t};
 }
 
-// Rows of a block of the backward.  More blocks hide more latency and cost
-// more partial rows; kBwdThreads threads per SM are in flight.
+// Rows of a block of the backward: as many blocks as the device holds at once
+// (by registers and by the ring of an FP32 stream, the larger one), so that
+// all start together and each writes one row of partial sums per sample.
 constexpr int kBwdSms = 148;
-constexpr int kBwdThreads = 768;
-int64_t norm_bwd_blocks(int64_t D) {
-    const RowShape s = row_shape(D);
-    return (int64_t)kBwdSms * std::max(1, std::min(8, kBwdThreads / s.threads));
-}
-int64_t norm_bwd_chunk(int64_t M, int64_t D) {
-    const RowShape s = row_shape(D);
+int64_t norm_bwd_chunk(int64_t M, int64_t D, bool mod) {
+    using namespace ft::norm;
+    const RowShape s = row_shape(D, true);
+    const int regs = !s.wide   ? kBwdRegs<1, false, false>
+                     : s.v == 1 ? (mod ? kBwdRegs<1, true, true> : kBwdRegs<1, true, false>)
+                                : (mod ? kBwdRegs<2, true, true> : kBwdRegs<2, true, false>);
+    const int ring = kBwdStages * (s.v == 1 ? Ring<kBwdSlots<float>, 1>::bytes(s.threads)
+                                            : Ring<kBwdSlots<float>, 2>::bytes(s.threads));
+    // each of an SM's four schedulers has 16384 registers for its warps
+    const int warps = 4 * (16384 / (32 * regs));
+    const int64_t blocks =
+        (int64_t)kBwdSms * std::max(1, std::min({warps / (s.threads / 32), 220 * 1024 / ring, 8}));
     const int64_t rows = s.wide ? 1 : s.threads / s.tpr;  // of a turn
-    const int64_t c = (M + norm_bwd_blocks(D) - 1) / norm_bwd_blocks(D);
+    const int64_t c = (M + blocks - 1) / blocks;
     return std::max<int64_t>(1, (c + rows - 1) / rows) * rows;
+}
+size_t norm_bwd_partials(int64_t M, int64_t D, int64_t B) {
+    const int64_t chunk = std::min(norm_bwd_chunk(M, D, false), norm_bwd_chunk(M, D, true));
+    return (size_t)((M + chunk - 1) / chunk + B) * 3 * (size_t)D;
 }
 
 ft_status check_norm(const ft_gated_norm* n) {
@@ -73,21 +83,68 @@ ft_status check_norm(const ft_gated_norm* n) {
     return FT_OK;
 }
 
-template <typename XT>
-ft_status launch_norm_fwd(const ft::norm::FwdParams& p, const RowShape& s, int grid, cudaStream_t st) {
-    if (!s.wide) return launch_overlapped(ft::norm::k_gated_norm_fwd<XT, 1, false>, grid, s.threads, 0, st, p);
-    if (s.v == 1) return launch_overlapped(ft::norm::k_gated_norm_fwd<XT, 1, true>, grid, s.threads, 0, st, p);
-    return launch_overlapped(ft::norm::k_gated_norm_fwd<XT, 2, true>, grid, s.threads, 0, st, p);
+// Launches `k` with `smem` bytes of dynamic shared memory per block, the grid
+// cut to the blocks that the device holds at once when `resident` is set.
+template <typename P>
+ft_status launch_norm(void (*k)(P), const P& p, int grid, bool resident, int threads, size_t smem, DevInfo* d,
+                      cudaStream_t st) {
+    if (smem > 32 * 1024)  // with the static part, above what a launch may take unasked
+        FT_TRY(cuda_ok(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)));
+    if (resident && grid > d->sms) {
+        int per_sm = 0;
+        FT_TRY(cuda_ok(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, threads, smem)));
+        // blocks with the same number of turns
+        grid = cdiv(grid, cdiv(grid, std::max(1, per_sm) * d->sms));
+    }
+    return launch_overlapped(k, grid, threads, smem, st, p);
 }
-template <typename XT, bool kAcc>
-ft_status launch_norm_bwd(const ft::norm::BwdParams& p, const RowShape& s, int grid, cudaStream_t st) {
-    if (!s.wide) return launch_overlapped(ft::norm::k_gated_norm_bwd<XT, 1, false, kAcc>, grid, s.threads, 0, st, p);
-    if (s.v == 1) return launch_overlapped(ft::norm::k_gated_norm_bwd<XT, 1, true, kAcc>, grid, s.threads, 0, st, p);
-    return launch_overlapped(ft::norm::k_gated_norm_bwd<XT, 2, true, kAcc>, grid, s.threads, 0, st, p);
+template <typename XT, int V, bool kWide, bool k32>
+ft_status launch_norm_fwd(const ft::norm::FwdParams& p, const RowShape& s, int grid, bool mod, DevInfo* d,
+                          cudaStream_t st) {
+    using namespace ft::norm;
+    const size_t smem = kFwdStages * Ring<kFwdSlots<XT>, V>::bytes(s.threads);
+    if constexpr (kWide)
+        if (mod) return launch_norm(k_gated_norm_fwd<XT, V, kWide, k32, true>, p, grid, true, s.threads, smem, d, st);
+    return launch_norm(k_gated_norm_fwd<XT, V, kWide, k32, false>, p, grid, true, s.threads, smem, d, st);
+}
+template <typename XT, int V, bool kWide, bool k32>
+ft_status launch_norm_bwd(const ft::norm::BwdParams& p, const RowShape& s, int grid, bool mod, DevInfo* d,
+                          cudaStream_t st) {
+    using namespace ft::norm;
+    const size_t smem = kBwdStages * Ring<kBwdSlots<XT>, V>::bytes(s.threads);
+    if constexpr (kWide)
+        if (mod) return launch_norm(k_gated_norm_bwd<XT, V, kWide, k32, true>, p, grid, false, s.threads, smem, d, st);
+    return launch_norm(k_gated_norm_bwd<XT, V, kWide, k32, false>, p, grid, false, s.threads, smem, d, st);
+}
+template <typename XT, bool k32>
+ft_status launch_norm(const ft::norm::FwdParams& p, const RowShape& s, int grid, DevInfo* d, cudaStream_t st) {
+    const bool mod = p.y && p.gate && p.scale && p.shift && !p.w && !p.bias && !p.w_post && p.post == FT_NORM_NONE;
+    if (!s.wide) return launch_norm_fwd<XT, 1, false, k32>(p, s, grid, false, d, st);
+    if (s.v == 1) return launch_norm_fwd<XT, 1, true, k32>(p, s, grid, mod, d, st);
+    if (s.v == 2) return launch_norm_fwd<XT, 2, true, k32>(p, s, grid, mod, d, st);
+    return launch_norm_fwd<XT, 4, true, k32>(p, s, grid, mod, d, st);
+}
+bool norm_bwd_mod(const ft::norm::BwdParams& p) {
+    return p.dh && p.dr && p.r && p.y && p.gate && p.scale && p.dx && p.dy && !p.w && !p.w_post &&
+           p.post == FT_NORM_NONE;
+}
+template <typename XT, bool k32>
+ft_status launch_norm(const ft::norm::BwdParams& p, const RowShape& s, int grid, DevInfo* d, cudaStream_t st) {
+    const bool mod = norm_bwd_mod(p);
+    if (!s.wide) return launch_norm_bwd<XT, 1, false, k32>(p, s, grid, false, d, st);
+    if (s.v == 1) return launch_norm_bwd<XT, 1, true, k32>(p, s, grid, mod, d, st);
+    return launch_norm_bwd<XT, 2, true, k32>(p, s, grid, mod, d, st);
+}
+template <typename P>
+ft_status launch_norm(const P& p, int xt, const RowShape& s, int grid, DevInfo* d, cudaStream_t st) {
+    if (xt == FT_F32) return p.p32 ? launch_norm<float, true>(p, s, grid, d, st) : launch_norm<float, false>(p, s, grid, d, st);
+    return p.p32 ? launch_norm<__nv_bfloat16, true>(p, s, grid, d, st)
+                 : launch_norm<__nv_bfloat16, false>(p, s, grid, d, st);
 }
 
 // ------------------------------------------------------------ rope
-constexpr int kRopeMaxBlocks = 148 * 8;
+constexpr int kRopeSms = 148;
+constexpr int kRopeMaxBlocks = kRopeSms * 8;
 
 ft_status check_rope(const ft_rope* R) {
     if (!R || R->M < 0 || R->S < 0 || R->Hq < 0 || R->Hk < 0 || R->n_axes < 1 || R->n_axes > 4)
@@ -129,7 +186,7 @@ ft::rope::Params rope_params(const ft_rope* R, const ft_heads* q, const ft_heads
     p.Hq = R->Hq;
     p.Hk = R->Hk;
     p.hd = R->hd;
-    p.heads = R->Hq + R->Hk + (v->p ? R->Hk : 0);
+    p.Hv = v->p ? R->Hk : 0;
     p.halves = R->layout == FT_ROPE_HALVES;
     p.norm = R->norm != FT_NORM_NONE;
     p.pos_f32 = R->post == FT_POS_F32;
@@ -152,14 +209,35 @@ ft::rope::Params rope_params(const ft_rope* R, const ft_heads* q, const ft_heads
     p.v = to_heads(v);
     return p;
 }
-// Blocks over rows, and over the heads of a row's table where rows alone do
-// not fill the device.
-dim3 rope_grid(const ft::rope::Params& p, int sms) {
-    const int rows = cdiv(p.M, ft::rope::kRows);
-    const int groups = ft::rope::kThreads / p.lanes;
-    const int most = std::max(1, cdiv((int64_t)std::min(p.M, ft::rope::kRows) * p.heads, groups));
-    const int y = rows >= 2 * sms ? 1 : std::max(1, std::min(most, 2 * sms / rows));
-    return dim3(std::max(1, std::min(rows, kRopeMaxBlocks)), y);
+// Warps over rows, as many as the device holds.  Rows are cut into up to
+// three slices of whole turns where that evens out the warps' shares by more
+// than forming the turns again costs (about a fifth of a row's work), into as
+// many as there are turns where rows do not fill the device.
+template <bool kBwd>
+int rope_grid(ft::rope::Params* p) {
+    using namespace ft::rope;
+    const int groups = 32 / p->lanes;
+    const int turns = cdiv(p->Hq, groups) + cdiv(p->Hk, groups) + cdiv(p->Hv, groups);
+    const int regs = p->norm ? kRegs<kBwd, true> : kRegs<kBwd, false>;
+    const int blocks = std::min(kRopeMaxBlocks, kRopeSms * (4 * (16384 / (32 * regs)) / kWarps));
+    const int64_t warps = (int64_t)blocks * kWarps;
+    p->slices = 1;
+    double best = 0.0;
+    for (int s = 1; s <= std::min(3, turns); ++s) {
+        const double cost = (double)((p->M * (int64_t)s + warps - 1) / warps) / s * (1.0 + 0.07 * (s - 1));
+        if (s == 1 || cost < best) best = cost, p->slices = s;
+    }
+    if (p->M * 3 < warps) p->slices = std::min<int>(turns, (int)(warps / p->M));
+    return (int)std::min<int64_t>(((int64_t)p->M * p->slices + kWarps - 1) / kWarps, blocks);
+}
+template <bool kBwd>
+ft_status launch_rope(const ft::rope::Params& p, int grid, cudaStream_t st) {
+    using namespace ft::rope;
+    auto* k = p.halves ? (p.norm ? k_qk_rope<kBwd, true, true> : k_qk_rope<kBwd, true, false>)
+                       : (p.norm ? k_qk_rope<kBwd, false, true> : k_qk_rope<kBwd, false, false>);
+    const size_t smem = p.norm ? kRingBytes<kBwd, true> : kRingBytes<kBwd, false>;
+    if (smem) FT_TRY(cuda_ok(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)));
+    return launch_overlapped(k, grid, kThreads, smem, st, p);
 }
 
 // ------------------------------------------------------------ adamw
@@ -169,7 +247,7 @@ constexpr int kAdamFew = 40, kAdamMany = 360;
 
 template <bool k8, int kMax>
 ft_status launch_adamw(const ft::adamw::Params<kMax>& p, DevInfo* d, cudaStream_t st) {
-    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(p.units, (int64_t)d->sms * 8));
+    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(p.units, (int64_t)d->sms * ft::adamw::kPerSm));
     LaunchTimer lt(KID_ADAMW, st);
     const ft_status s = launch_overlapped(ft::adamw::k_adamw<k8, kMax>, grid, 32 * ft::adamw::kWarps, 0, st, p);
     lt.stop();
@@ -192,6 +270,8 @@ ft_status adamw_group(const ft_adamw_tensor* t, int64_t begin, int64_t end, cons
     p.grad_scale = grad_scale;
     p.step = reinterpret_cast<long long*>(step);
     p.last = last;
+    // 1e-18 is more than the square root of any subnormal v / (1 - beta2^t)
+    p.exact = !(h->eps >= 1e-16);
     for (int64_t i = begin; i < end; ++i) {
         const ft_adamw_tensor& a = t[i];
         if (a.n == 0) continue;
@@ -206,7 +286,8 @@ ft_status adamw_group(const ft_adamw_tensor* t, int64_t begin, int64_t end, cons
         q.n = a.n;
         q.wd = a.weight_decay;
         q.g16 = a.gt == FT_BF16;
-        q.vec = al16(a.p) && al16(a.p16) && al16(a.grad) && (k8 ? al8(a.m) && al8(a.v) : al16(a.m) && al16(a.v));
+        q.vec = al16(a.p) && al8(a.p16) && (q.g16 ? al8(a.grad) : al16(a.grad)) &&
+                (k8 ? al4(a.m) && al4(a.v) : al16(a.m) && al16(a.v));
         q.first = p.units;
         p.units += (unsigned)((a.n + ft::adamw::kUnit - 1) / ft::adamw::kUnit);
     }
@@ -219,8 +300,7 @@ extern "C" {
 
 size_t ft_gated_norm_workspace_bytes(int64_t M, int64_t D, int64_t B) {
     if (M < 0 || M > kMaxRows || D < 8 || D % 8 || D > kNormMaxD || B < 1 || B > kMaxRows) return 0;
-    const int64_t chunk = norm_bwd_chunk(M, D);
-    return (size_t)((M + chunk - 1) / chunk + B) * 3 * (size_t)D * sizeof(float);
+    return (norm_bwd_partials(M, D, B) + (size_t)B * 3 * (size_t)D) * sizeof(float);
 }
 
 ft_status ft_gated_norm_fwd(const ft_gated_norm* n, const void* x, int64_t ldx, const void* y, int64_t ldy, void* r,
@@ -241,7 +321,7 @@ ft_status ft_gated_norm_fwd(const ft_gated_norm* n, const void* x, int64_t ldx, 
     DevInfo* d;
     FT_TRY(device_info(&d));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const RowShape s = row_shape(n->D);
+    const RowShape s = row_shape(n->D, false);
     ft::norm::FwdParams p = {};
     p.M = (int)n->M;
     p.D = (int)n->D;
@@ -276,10 +356,9 @@ ft_status ft_gated_norm_fwd(const ft_gated_norm* n, const void* x, int64_t ldx, 
     p.amax = amax_h;
     p.tpr = s.tpr;
     const int per = s.wide ? 1 : s.threads / s.tpr;
-    const int grid = (int)std::min<int64_t>(cdiv(n->M, per), (int64_t)d->sms * std::max(1, 1536 / s.threads));
+    const int grid = cdiv(n->M, per);
     LaunchTimer lt(KID_NORM_FWD, st);
-    const ft_status e = n->xt == FT_F32 ? launch_norm_fwd<float>(p, s, grid, st)
-                                        : launch_norm_fwd<__nv_bfloat16>(p, s, grid, st);
+    const ft_status e = launch_norm(p, n->xt, s, grid, d, st);
     lt.stop();
     return e;
 }
@@ -312,7 +391,7 @@ ft_status ft_gated_norm_bwd(const ft_gated_norm* n, const void* dh, int64_t lddh
         !al4(g->dscale) || !al4(g->dshift) || !al4(g->dw_post) || !al4(g->dw) || !al4(g->dbias))
         return FT_ERR_ALIGN;
     const bool acc = need_s || need_t;
-    if (acc && rows) {
+    if (acc) {
         if (!ws || ws_bytes < ft_gated_norm_workspace_bytes(n->M, n->D, n->B)) return FT_ERR_WORKSPACE;
         if (!al16(ws)) return FT_ERR_ALIGN;
     }
@@ -320,9 +399,8 @@ ft_status ft_gated_norm_bwd(const ft_gated_norm* n, const void* dh, int64_t lddh
     DevInfo* d;
     FT_TRY(device_info(&d));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const RowShape s = row_shape(n->D);
-    const int64_t chunk = norm_bwd_chunk(n->M, n->D);
-    const int chunks = (int)((n->M + chunk - 1) / chunk);
+    const RowShape s = row_shape(n->D, true);
+    int64_t chunk = 1;
     if (rows) {
         ft::norm::BwdParams p = {};
         p.M = (int)n->M;
@@ -358,15 +436,12 @@ ft_status ft_gated_norm_bwd(const ft_gated_norm* n, const void* dh, int64_t lddh
         p.partial = static_cast<float*>(ws);
         p.need_s = need_s;
         p.need_t = need_t;
+        chunk = norm_bwd_chunk(n->M, n->D, norm_bwd_mod(p));
         p.chunk = (int)chunk;
         p.tpr = s.tpr;
+        const int chunks = (int)((n->M + chunk - 1) / chunk);
         LaunchTimer lt(KID_NORM_BWD, st);
-        ft_status e;
-        if (n->xt == FT_F32)
-            e = acc ? launch_norm_bwd<float, true>(p, s, chunks, st) : launch_norm_bwd<float, false>(p, s, chunks, st);
-        else
-            e = acc ? launch_norm_bwd<__nv_bfloat16, true>(p, s, chunks, st)
-                    : launch_norm_bwd<__nv_bfloat16, false>(p, s, chunks, st);
+        const ft_status e = launch_norm(p, n->xt, s, chunks, d, st);
         lt.stop();
         FT_TRY(e);
     }
@@ -377,7 +452,6 @@ ft_status ft_gated_norm_bwd(const ft_gated_norm* n, const void* dh, int64_t lddh
     q.B = (int)n->B;
     q.S = (int)(n->M / n->B);
     q.chunk = (int)chunk;
-    q.chunks = chunks;
     q.offsets = n->offsets;
     q.alpha = n->alpha;
     q.p32 = n->pt == FT_F32;
@@ -397,11 +471,16 @@ ft_status ft_gated_norm_bwd(const ft_gated_norm* n, const void* dh, int64_t lddh
     q.dbias = g->dbias;
     q.need_s = need_s;
     q.need_t = need_t;
-    q.all_samples = g->dw_post || g->dw || g->dbias;
-    const dim3 grid(cdiv(n->D, 32), q.all_samples ? 1 : (unsigned)std::min<int64_t>(n->B, 32768));
+    if (g->dw_post || g->dw || g->dbias) q.sums = static_cast<float*>(ws) + norm_bwd_partials(n->M, n->D, n->B);
     LaunchTimer lt(KID_NORM_REDUCE, st);
-    const ft_status e = launch_overlapped(ft::norm::k_gated_norm_reduce, grid, 32 * ft::norm::kReduceGroups, 0, st, q);
+    ft_status e = launch_overlapped(ft::norm::k_gated_norm_reduce,
+                                    dim3(cdiv(n->D, 32), (unsigned)std::min<int64_t>(n->B, 32768)),
+                                    32 * ft::norm::kReduceGroups, 0, st, q);
     lt.stop();
+    if (e != FT_OK || !q.sums) return e;
+    LaunchTimer lt2(KID_NORM_WEIGHTS, st);
+    e = launch_overlapped(ft::norm::k_gated_norm_weights, cdiv(n->D, 64), 64, 0, st, q);
+    lt2.stop();
     return e;
 }
 
@@ -413,12 +492,15 @@ ft_status ft_gelu_bwd_bf16(const void* y, const void* dh, void* dy, int64_t n, f
     DevInfo* d;
     FT_TRY(device_info(&d));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int grid = (int)std::min<int64_t>((n / 8 + 255) / 256, (int64_t)d->sms * 8);
+    // a table pays once a block looks up more slopes than its 4096 entries
+    const bool table = n >= (int64_t)d->sms * ft::gelub::kTab;
+    const int threads = table ? ft::gelub::kThreads : 128;
+    const int grid = (int)std::min<int64_t>((n / 8 + threads - 1) / threads, (int64_t)d->sms * (table ? 1 : 16));
     LaunchTimer lt(KID_GELU_BWD, st);
-    const ft_status e = launch_overlapped_args(ft::gelub::k_gelu_bwd_bf16, grid, 256, 0, st,
-                                               static_cast<const __nv_bfloat16*>(y),
-                                               static_cast<const __nv_bfloat16*>(dh), static_cast<__nv_bfloat16*>(dy), n,
-                                               amax_dy);
+    const ft_status e = launch_overlapped_args(
+        table ? ft::gelub::k_gelu_bwd_bf16<true> : ft::gelub::k_gelu_bwd_bf16<false>, grid, threads, 0, st,
+        static_cast<const __nv_bfloat16*>(y), static_cast<const __nv_bfloat16*>(dh), static_cast<__nv_bfloat16*>(dy), n,
+        amax_dy);
     lt.stop();
     return e;
 }
@@ -433,15 +515,15 @@ ft_status ft_qk_rope_fwd(const ft_rope* R, const void* qkv, int64_t ld, const ft
     if (ld < ((int64_t)R->Hq + 2 * (int64_t)R->Hk) * R->hd) return FT_ERR_SHAPE;
     if (!rows_al16(qkv, ld, 2)) return FT_ERR_ALIGN;
     ft::rope::Params p = rope_params(R, q, k, v);
-    if (R->M == 0 || p.heads == 0) return FT_OK;
+    if (R->M == 0 || p.Hq + p.Hk + p.Hv == 0) return FT_OK;
     DevInfo* d;
     FT_TRY(device_info(&d));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     p.x = static_cast<const __nv_bfloat16*>(qkv);
     p.ld = ld;
     LaunchTimer lt(KID_ROPE_FWD, st);
-    const ft_status e =
-        launch_overlapped(ft::rope::k_qk_rope<false>, rope_grid(p, d->sms), ft::rope::kThreads, 0, st, p);
+    const int grid = rope_grid<false>(&p);
+    const ft_status e = launch_rope<false>(p, grid, st);
     lt.stop();
     return e;
 }
@@ -467,7 +549,7 @@ ft_status ft_qk_rope_bwd(const ft_rope* R, const ft_heads* dq, const ft_heads* d
     if (dw && (!ws || ws_bytes < ft_qk_rope_workspace_bytes(R->M, R->hd))) return FT_ERR_WORKSPACE;
     if (dw && !al4(ws)) return FT_ERR_ALIGN;
     ft::rope::Params p = rope_params(R, dq, dk, dv);
-    const bool work = R->M > 0 && p.heads > 0;
+    const bool work = R->M > 0 && p.Hq + p.Hk + p.Hv > 0;
     if (!work && !dw) return FT_OK;
     DevInfo* d;
     FT_TRY(device_info(&d));
@@ -480,16 +562,15 @@ ft_status ft_qk_rope_bwd(const ft_rope* R, const ft_heads* dq, const ft_heads* d
         p.lddx = lddqkv;
         p.amax = amax;
         p.partial = dw ? static_cast<float*>(ws) : nullptr;
-        const dim3 grid = rope_grid(p, d->sms);
-        blocks = (int)(grid.x * grid.y);
+        blocks = rope_grid<true>(&p);
         LaunchTimer lt(KID_ROPE_BWD, st);
-        const ft_status e = launch_overlapped(ft::rope::k_qk_rope<true>, grid, ft::rope::kThreads, 0, st, p);
+        const ft_status e = launch_rope<true>(p, blocks, st);
         lt.stop();
         FT_TRY(e);
     }
     if (!dw) return FT_OK;
     LaunchTimer lt(KID_ROPE_REDUCE, st);
-    const ft_status e = launch_overlapped_args(ft::rope::k_qk_rope_reduce, cdiv(2 * R->hd, 8), 256, 0, st,
+    const ft_status e = launch_overlapped_args(ft::rope::k_qk_rope_reduce, cdiv(2 * R->hd, 32), 1024, 0, st,
                                                static_cast<const float*>(ws), blocks, (int)R->hd, dw_q, dw_k);
     lt.stop();
     return e;
@@ -535,10 +616,13 @@ ft_status ft_adamw_decode(const void* codes, const float* scales, int64_t n, int
     DevInfo* d;
     FT_TRY(device_info(&d));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int grid = (int)std::min<int64_t>((n + 255) / 256, (int64_t)d->sms * 16);
+    const int vec = al4(codes) && al16(out);
+    const int64_t blocks = (n + ft::adamw::kBlock - 1) / ft::adamw::kBlock;
+    const int grid = (int)std::min<int64_t>((blocks + 7) / 8, (int64_t)d->sms * 6);
     LaunchTimer lt(KID_ADAMW_DECODE, st);
     const ft_status e = launch_overlapped_args(ft::adamw::k_adamw_decode, grid, 256, 0, st,
-                                               static_cast<const uint8_t*>(codes), scales, (long long)n, second, out);
+                                               static_cast<const uint8_t*>(codes), scales, (long long)n, second, out,
+                                               vec);
     lt.stop();
     return e;
 }

@@ -21,9 +21,10 @@
 namespace ft {
 namespace adamw {
 
-constexpr int kBlock = 256;            // elements that share a scale
+constexpr int kBlock = 256;  // elements that share a scale; a warp's at a time, eight per lane
 constexpr int kWarps = 8;
-constexpr int kUnit = kBlock * kWarps;  // elements of one turn of a block of threads
+constexpr int kUnit = kBlock * kWarps;  // elements that a block of threads takes at a time, within one tensor
+constexpr int kPerSm = 5;               // blocks of threads that an SM holds
 
 struct Tensor {
     float* p;
@@ -42,6 +43,7 @@ template <int kMax>
 struct Params {
     int count, last;  // last: this launch ends the step
     unsigned units;
+    bool exact;  // eps does not cover what the fast division leaves out
     float b1, c1, b2, c2, eps;  // c = 1 - b, rounded from double
     double lr, log_b1, log_b2;
     const float* lr_dev;
@@ -50,27 +52,180 @@ struct Params {
     Tensor t[kMax];
 };
 
-__device__ __forceinline__ float decode_m(int c, float top) {
-    return __fmul_rn(__fmul_rn((float)(c * abs(c)), 1.0f / 16129.0f), top);
+// A byte of w as the float 2^23 + byte: its bits are the byte under the
+// exponent of 2^23.
+__device__ __forceinline__ float byte_as_float(uint32_t w, int i) {
+    return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7650u | (uint32_t)i));
 }
-__device__ __forceinline__ float decode_v(int c, float top) {
-    const float r = __fmul_rn((float)(c * c), 1.0f / 65025.0f);
-    return __fmul_rn(__fmul_rn(r, r), top);
+// The values of the codes in bytes i, i + 1 of w (m: two's complement, v:
+// unsigned).
+__device__ __forceinline__ float2 decode_m(uint32_t w, int i, float top) {
+    w ^= 0x80808080u;  // 2^23 + (c + 128), exact
+    const float2 c = add2(make_float2(byte_as_float(w, i), byte_as_float(w, i + 1)), both(-8388736.0f));
+    const float2 q = mul2(c, make_float2(fabsf(c.x), fabsf(c.y)));
+    return mul2(mul2(q, both(1.0f / 16129.0f)), both(top));
+}
+__device__ __forceinline__ float2 decode_v(uint32_t w, int i, float top) {
+    const float2 c = add2(make_float2(byte_as_float(w, i), byte_as_float(w, i + 1)), both(-8388608.0f));
+    const float2 r = mul2(mul2(c, c), both(1.0f / 65025.0f));
+    return mul2(mul2(r, r), both(top));
 }
 __device__ __forceinline__ float recip_top(float top) { return top >= 1.17549435e-38f ? __frcp_rn(top) : 0.0f; }
-__device__ __forceinline__ int encode_m(float m, float inv) {
-    const int c = __float2int_rn(__fmul_rn(__fsqrt_rn(__fmul_rn(fabsf(m), inv)), 127.0f));
-    return m < 0.0f ? -c : c;
+
+// Codes as defined: every step rounded once.
+__device__ __forceinline__ float scaled_m(float m, float inv) {
+    return copysignf(__fmul_rn(__fsqrt_rn(__fmul_rn(fabsf(m), inv)), 127.0f), m);
 }
-__device__ __forceinline__ int encode_v(float v, float inv) {
-    return __float2int_rn(__fmul_rn(__fsqrt_rn(__fsqrt_rn(__fmul_rn(v, inv))), 255.0f));
+__device__ __forceinline__ float scaled_v(float v, float inv) {
+    return __fmul_rn(__fsqrt_rn(__fsqrt_rn(__fmul_rn(v, inv))), 255.0f);
 }
-// the largest of a and b, NaN if one of them is
-__device__ __forceinline__ float max_nan(float a, float b) { return a != a || a > b ? a : b; }
+// Hardware square root and reciprocal: to 2^-23, 0 (infinity) for what is
+// below 2^-126.
+__device__ __forceinline__ float2 sqrt_near(float2 x) {
+    asm("sqrt.approx.ftz.f32 %0, %0;" : "+f"(x.x));
+    asm("sqrt.approx.ftz.f32 %0, %0;" : "+f"(x.y));
+    return x;
+}
+__device__ __forceinline__ float2 recip_near(float2 x) {
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(x.x));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(x.y));
+    return x;
+}
+// With hardware square roots the scaled values are off by less than kNear:
+// m's, up to 127, by one root, the defined root's own rounding and two
+// products' (2.5 2^-23 127 = 3.8e-5), v's, up to 255, by two roots, the second
+// halving the first's error (3.3 2^-23 255 = 1.0e-4).  Where a value is that
+// close to the border of two codes, the lane's eight are taken by the
+// definition (one warp in fourteen has one).
+constexpr float kNear = 1.25e-4f;
+
+// Adding 1.5 2^23 rounds to the nearest integer (ties to even) and leaves it
+// in the low byte, negative ones in two's complement.  `edge` grows to the
+// largest distance from the integer.
+__device__ __forceinline__ float2 rounded(float2 t, float& edge) {
+    const float2 r = add2(t, both(12582912.0f));
+    const float2 n = add2(r, both(-12582912.0f));
+    const float2 d = fma2(n, both(-1.0f), t);
+    edge = fmaxf(edge, fmaxf(fabsf(d.x), fabsf(d.y)));
+    return r;
+}
+__device__ __forceinline__ uint32_t low_bytes(float2 a, float2 b) {
+    return __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
+                       __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
+}
+template <bool kSecond>
+__device__ __noinline__ uint2 codes_defined(float2 a, float2 b, float2 c, float2 d, float inv) {
+    float2 t[4] = {a, b, c, d};
+    float edge = 0.0f;
+    for (int i = 0; i < 4; ++i) {
+        t[i] = kSecond ? make_float2(scaled_v(t[i].x, inv), scaled_v(t[i].y, inv))
+                       : make_float2(scaled_m(t[i].x, inv), scaled_m(t[i].y, inv));
+        t[i] = rounded(t[i], edge);
+    }
+    return make_uint2(low_bytes(t[0], t[1]), low_bytes(t[2], t[3]));
+}
+template <bool kSecond>
+__device__ __forceinline__ uint2 codes(const float2 (&x)[4], float inv, bool defined) {
+    float2 t[4];
+    float edge = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (kSecond) {
+            t[i] = mul2(sqrt_near(sqrt_near(mul2(x[i], both(inv)))), both(255.0f));
+        } else {
+            t[i] = mul2(sqrt_near(mul2(make_float2(fabsf(x[i].x), fabsf(x[i].y)), both(inv))), both(127.0f));
+            t[i] = make_float2(copysignf(t[i].x, x[i].x), copysignf(t[i].y, x[i].y));
+        }
+        t[i] = rounded(t[i], edge);
+    }
+    if (defined || !(edge < 0.5f - kNear)) return codes_defined<kSecond>(x[0], x[1], x[2], x[3], inv);
+    return make_uint2(low_bytes(t[0], t[1]), low_bytes(t[2], t[3]));
+}
+
+// The sum of two products that were each rounded: a two-lane sum would be
+// contracted with the two-lane product before it.
+__device__ __forceinline__ float2 sum_of(float2 a, float2 b) {
+    return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
+}
+
+// A lane's eight values of a block: 4 l .. 4 l + 3 and the same 128 further,
+// so that every access of a warp is one run of bytes whatever the type.  at:
+// the lane's first; vec: all are there and aligned, else those before `left`.
+constexpr int kHalf = kBlock / 2;
+__device__ __forceinline__ bool there(int i, int left) { return (i & 3) + (i >> 2) * kHalf < left; }
+__device__ __forceinline__ void load_pairs(float2 (&f)[4], const float* at, bool vec, int left) {
+    if (vec) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint4 r = ld_stream_v4(at + h * kHalf);
+            f[2 * h] = make_float2(__uint_as_float(r.x), __uint_as_float(r.y));
+            f[2 * h + 1] = make_float2(__uint_as_float(r.z), __uint_as_float(r.w));
+        }
+    } else {
+        float t[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = there(i, left) ? at[(i & 3) + (i >> 2) * kHalf] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = make_float2(t[2 * i], t[2 * i + 1]);
+    }
+}
+__device__ __forceinline__ void load_pairs(float2 (&f)[4], const __nv_bfloat16* at, bool vec, int left) {
+    if (vec) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint2 r = ld_stream_v2(at + h * kHalf);
+            f[2 * h] = make_float2(bf16_lo(r.x), bf16_hi(r.x));
+            f[2 * h + 1] = make_float2(bf16_lo(r.y), bf16_hi(r.y));
+        }
+    } else {
+        float t[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            t[i] = there(i, left) ? __bfloat162float(at[(i & 3) + (i >> 2) * kHalf]) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = make_float2(t[2 * i], t[2 * i + 1]);
+    }
+}
+__device__ __forceinline__ void put_quad(float* p, float2 a, float2 b) {
+    *reinterpret_cast<float4*>(p) = make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ void put_quad(__nv_bfloat16* p, float2 a, float2 b) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(a.x, a.y), pack_bf16(b.x, b.y));
+}
+template <typename T>
+__device__ __forceinline__ void store_pairs(T* at, const float2 (&f)[4], bool vec, int left) {
+    if (vec) {
+        put_quad(at, f[0], f[1]);
+        put_quad(at + kHalf, f[2], f[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (there(i, left)) at[(i & 3) + (i >> 2) * kHalf] = (T)(i & 1 ? f[i >> 1].y : f[i >> 1].x);
+    }
+}
+__device__ __forceinline__ uint2 load_codes(const uint8_t* at, bool vec, int left) {
+    if (vec) return make_uint2(*reinterpret_cast<const uint32_t*>(at), *reinterpret_cast<const uint32_t*>(at + kHalf));
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (there(i, left)) w[i >> 2] |= (uint32_t)at[(i & 3) + (i >> 2) * kHalf] << (8 * (i & 3));
+    return make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ void store_codes(uint8_t* at, uint2 c, bool vec, int left) {
+    if (vec) {
+        *reinterpret_cast<uint32_t*>(at) = c.x;
+        *reinterpret_cast<uint32_t*>(at + kHalf) = c.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (there(i, left)) at[(i & 3) + (i >> 2) * kHalf] = (uint8_t)((i < 4 ? c.x : c.y) >> (8 * (i & 3)));
+    }
+}
 
 template <bool k8, int kMax>
-__global__ void __launch_bounds__(32 * kWarps) k_adamw(const __grid_constant__ Params<kMax> p) {
+__global__ void __launch_bounds__(32 * kWarps, kPerSm) k_adamw(const __grid_constant__ Params<kMax> p) {
     __shared__ float coef[2];
+    grid_dep_launch();
     grid_dep_wait();
     const float gs = p.grad_scale ? *p.grad_scale : 1.0f;
     const double lr = p.lr_dev ? (double)*p.lr_dev : p.lr;
@@ -83,134 +238,84 @@ __global__ void __launch_bounds__(32 * kWarps) k_adamw(const __grid_constant__ P
     __syncthreads();
     const float rate = coef[0], rc2 = coef[1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int tensor = 0;
     for (unsigned unit = blockIdx.x; unit < p.units; unit += gridDim.x) {
-        // the last tensor whose first unit is not above this one
-        int lo = 0, hi = p.count - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (p.t[mid].first <= unit)
-                lo = mid;
-            else
-                hi = mid - 1;
-        }
-        const Tensor& T = p.t[lo];
-        const long long block = (long long)(unit - T.first) * kWarps + warp;
-        const long long at = block * kBlock + lane * 8;
-        if (block * kBlock >= T.n) continue;
-        const int live = (int)max(0ll, min(8ll, T.n - at));
-        const bool vec = T.vec && live == 8;
-        float g[8] = {}, w[8] = {}, m[8] = {}, v[8] = {};
-        float mtop = 0.0f, vtop = 0.0f;
-        if (k8) {
-            mtop = T.ms[block];
-            vtop = T.vs[block];
-        }
-        if (vec) {
-            if (T.g16) {
-                unpack8(ld_stream_v4(static_cast<const __nv_bfloat16*>(T.g) + at), g);
-            } else {
-                Raw8<float> r;
-                load8(r, static_cast<const float*>(T.g) + at);
-                unpack8(r, g);
-            }
-            if (T.p) {
-                Raw8<float> r;
-                load8(r, T.p + at);
-                unpack8(r, w);
-            } else {
-                unpack8(ld_stream_v4(T.p16 + at), w);
-            }
-            if (k8) {
-                const uint2 a = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(T.m) + at);
-                const uint2 b = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(T.v) + at);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    m[i] = decode_m((int)(int8_t)((i < 4 ? a.x : a.y) >> (8 * (i & 3))), mtop);
-                    v[i] = decode_v((int)(((i < 4 ? b.x : b.y) >> (8 * (i & 3))) & 255u), vtop);
-                }
-            } else {
-                Raw8<float> r;
-                load8(r, static_cast<const float*>(T.m) + at);
-                unpack8(r, m);
-                load8(r, static_cast<const float*>(T.v) + at);
-                unpack8(r, v);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (i >= live) continue;
-                g[i] = T.g16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(T.g)[at + i])
-                             : static_cast<const float*>(T.g)[at + i];
-                w[i] = T.p ? T.p[at + i] : __bfloat162float(T.p16[at + i]);
-                m[i] = k8 ? decode_m(static_cast<const int8_t*>(T.m)[at + i], mtop)
-                          : static_cast<const float*>(T.m)[at + i];
-                v[i] = k8 ? decode_v(static_cast<const uint8_t*>(T.v)[at + i], vtop)
-                          : static_cast<const float*>(T.v)[at + i];
-            }
-        }
+        while (tensor + 1 < p.count && p.t[tensor + 1].first <= unit) ++tensor;
+        const Tensor& T = p.t[tensor];
+        const long long n = T.n;
         const float decay = (float)(1.0 - lr * (double)T.wd);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float gi = __fmul_rn(g[i], gs);
-            m[i] = __fadd_rn(__fmul_rn(m[i], p.b1), __fmul_rn(gi, p.c1));
-            v[i] = __fadd_rn(__fmul_rn(v[i], p.b2), __fmul_rn(__fmul_rn(gi, p.c2), gi));
-            w[i] = fmaf(-rate, __fdiv_rn(m[i], fmaf(__fsqrt_rn(v[i]), rc2, p.eps)), w[i] * decay);
-        }
-        uint2 cm = make_uint2(0, 0), cv = make_uint2(0, 0);
-        if (k8) {
-            mtop = vtop = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < live) {
-                    mtop = max_nan(fabsf(m[i]), mtop);
-                    vtop = max_nan(v[i], vtop);
-                }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                mtop = max_nan(__shfl_xor_sync(0xFFFFFFFFu, mtop, o), mtop);
-                vtop = max_nan(__shfl_xor_sync(0xFFFFFFFFu, vtop, o), vtop);
-            }
-            // a non-finite block: no code can stand for its values
-            const float bad = __int_as_float(0x7FC00000);
-            if (!(mtop <= 3.4028234e38f)) mtop = bad;
-            if (!(vtop <= 3.4028234e38f)) vtop = bad;
-            const float mi = recip_top(mtop), vi = recip_top(vtop);
-            uint32_t am[2] = {0, 0}, av[2] = {0, 0};
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                am[i >> 2] |= (uint32_t)(uint8_t)encode_m(m[i], mi) << (8 * (i & 3));
-                av[i >> 2] |= (uint32_t)(uint8_t)encode_v(v[i], vi) << (8 * (i & 3));
-            }
-            cm = make_uint2(am[0], am[1]);
-            cv = make_uint2(av[0], av[1]);
-            if (lane == 0) {
-                T.ms[block] = mtop;
-                T.vs[block] = vtop;
-            }
-        }
-        if (vec) {
-            if (T.p) store8(T.p + at, w);
-            if (T.p16) store8(T.p16 + at, w);
+        const bool g16 = T.g16, aligned = T.vec;
+        float* const tp = T.p;
+        __nv_bfloat16* const tp16 = T.p16;
+        const long long block = (long long)(unit - T.first) * kWarps + warp;
+        if (block * kBlock < n) {
+            const long long at = block * kBlock + lane * 4;
+            const int live = (int)max(0ll, min((long long)kBlock, n - at));  // of the block from this lane's first on
+            const bool vec = aligned && live >= kHalf + 4;
+            float2 g[4], w[4], m[4], v[4];
+            float mtop = 0.0f, vtop = 0.0f;
+            if (g16)
+                load_pairs(g, static_cast<const __nv_bfloat16*>(T.g) + at, vec, live);
+            else
+                load_pairs(g, static_cast<const float*>(T.g) + at, vec, live);
+            if (tp)
+                load_pairs(w, tp + at, vec, live);
+            else
+                load_pairs(w, tp16 + at, vec, live);
             if (k8) {
-                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(T.m) + at) = cm;
-                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(T.v) + at) = cv;
-            } else {
-                store8(static_cast<float*>(T.m) + at, m);
-                store8(static_cast<float*>(T.v) + at, v);
-            }
-        } else {
+                mtop = T.ms[block];
+                vtop = T.vs[block];
+                const uint2 a = load_codes(static_cast<const uint8_t*>(T.m) + at, vec, live);
+                const uint2 b = load_codes(static_cast<const uint8_t*>(T.v) + at, vec, live);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (i >= live) continue;
-                if (T.p) T.p[at + i] = w[i];
-                if (T.p16) T.p16[at + i] = __float2bfloat16_rn(w[i]);
-                if (k8) {
-                    static_cast<uint8_t*>(T.m)[at + i] = (uint8_t)((i < 4 ? cm.x : cm.y) >> (8 * (i & 3)));
-                    static_cast<uint8_t*>(T.v)[at + i] = (uint8_t)((i < 4 ? cv.x : cv.y) >> (8 * (i & 3)));
-                } else {
-                    static_cast<float*>(T.m)[at + i] = m[i];
-                    static_cast<float*>(T.v)[at + i] = v[i];
+                for (int i = 0; i < 4; ++i) {
+                    m[i] = decode_m(i < 2 ? a.x : a.y, 2 * (i & 1), mtop);
+                    v[i] = decode_v(i < 2 ? b.x : b.y, 2 * (i & 1), vtop);
                 }
+            } else {
+                load_pairs(m, static_cast<const float*>(T.m) + at, vec, live);
+                load_pairs(v, static_cast<const float*>(T.v) + at, vec, live);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                g[i] = mul2(g[i], both(gs));
+                m[i] = sum_of(mul2(m[i], both(p.b1)), mul2(g[i], both(p.c1)));
+                v[i] = sum_of(mul2(v[i], both(p.b2)), mul2(mul2(g[i], both(p.c2)), g[i]));
+                // a few ulp of the step itself are far below the weight's;
+                // a subnormal v counts as zero next to eps
+                float2 u = mul2(m[i], recip_near(fma2(sqrt_near(v[i]), both(rc2), both(p.eps))));
+                if (p.exact)
+                    u = make_float2(m[i].x / fmaf(sqrtf(v[i].x), rc2, p.eps), m[i].y / fmaf(sqrtf(v[i].y), rc2, p.eps));
+                w[i] = fma2(u, both(-rate), mul2(w[i], both(decay)));
+            }
+            if (tp) store_pairs(tp + at, w, vec, live);
+            if (tp16) store_pairs(tp16 + at, w, vec, live);
+            if (k8) {
+                // magnitudes order like their bits, NaN above infinity; what
+                // is not there is zero
+                uint32_t mb = 0, vb = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    mb = max(mb, max(__float_as_uint(m[i].x) & 0x7FFFFFFFu, __float_as_uint(m[i].y) & 0x7FFFFFFFu));
+                    vb = max(vb, max(__float_as_uint(v[i].x) & 0x7FFFFFFFu, __float_as_uint(v[i].y) & 0x7FFFFFFFu));
+                }
+                mb = __reduce_max_sync(0xFFFFFFFFu, mb);
+                vb = __reduce_max_sync(0xFFFFFFFFu, vb);
+                // a non-finite block: no code can stand for its values
+                const bool bad = max(mb, vb) >= 0x7F800000u;
+                mtop = __uint_as_float(mb >= 0x7F800000u ? 0x7FC00000u : mb);
+                vtop = __uint_as_float(vb >= 0x7F800000u ? 0x7FC00000u : vb);
+                const uint2 cm = codes<false>(m, recip_top(mtop), bad);
+                const uint2 cv = codes<true>(v, recip_top(vtop), bad);
+                store_codes(static_cast<uint8_t*>(T.m) + at, cm, vec, live);
+                store_codes(static_cast<uint8_t*>(T.v) + at, cv, vec, live);
+                if (lane == 0) {
+                    T.ms[block] = mtop;
+                    T.vs[block] = vtop;
+                }
+            } else {
+                store_pairs(static_cast<float*>(T.m) + at, m, vec, live);
+                store_pairs(static_cast<float*>(T.v) + at, v, vec, live);
             }
         }
     }
@@ -228,12 +333,40 @@ __global__ void __launch_bounds__(32 * kWarps) k_adamw(const __grid_constant__ P
     }
 }
 
+// A block of codes per warp at a time, four of them in flight.
 __global__ void __launch_bounds__(256) k_adamw_decode(const uint8_t* codes, const float* scales, long long n,
-                                                      int second, float* out) {
+                                                      int second, float* out, int aligned) {
+    constexpr int U = 4;
+    const int lane = threadIdx.x & 31;
+    grid_dep_launch();
     grid_dep_wait();
-    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (long long)gridDim.x * blockDim.x) {
-        const float top = __ldg(scales + i / kBlock);
-        out[i] = second ? decode_v(codes[i], top) : decode_m((int8_t)codes[i], top);
+    const long long blocks = (n + kBlock - 1) / kBlock, step = (long long)gridDim.x * (blockDim.x >> 5);
+    for (long long b = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); b < blocks; b += U * step) {
+        uint2 c[U];
+        float top[U];
+        int live[U];
+        bool vec[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const long long at = (b + u * step) * kBlock + lane * 4;
+            live[u] = (int)max(0ll, min((long long)kBlock, n - at));
+            vec[u] = aligned && live[u] >= kHalf + 4;
+            if (b + u * step < blocks) {
+                c[u] = load_codes(codes + at, vec[u], live[u]);
+                top[u] = __ldg(scales + b + u * step);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (b + u * step >= blocks) break;
+            float2 f[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t w = k < 2 ? c[u].x : c[u].y;
+                f[k] = second ? decode_v(w, 2 * (k & 1), top[u]) : decode_m(w, 2 * (k & 1), top[u]);
+            }
+            store_pairs(out + (b + u * step) * kBlock + lane * 4, f, vec[u], live[u]);
+        }
     }
 }
 

@@ -15,9 +15,9 @@
 //     dw = sum_b (1 + scale_b) S1_b, dbias = sum_b (1 + scale_b) S0_b,
 //     dw_post = sum_b alpha gate_b T_b
 //
-// A row stays in registers between its one load and its one store, the
-// variance is taken about the mean (no cancellation), and the next row's
-// loads are in flight while a row is reduced.  HBM bounds both kernels: 8 B
+// A row stays on chip between its one load and its one store, the variance is
+// taken about the mean (no cancellation), and the next rows' loads are in
+// flight while a row is reduced.  HBM bounds both kernels: 8 B
 // per element forward (x, y, r, h in bf16), 12 B backward (dh, dr, r, y, dx,
 // dy).
 #pragma once
@@ -94,437 +94,455 @@ __device__ __forceinline__ int sample_of(int row, const int32_t* offsets, int B,
 }
 
 // Sum over the threads of a row: within groups of `tpr` lanes (kWide false)
-// or over the block (kWide true; `red` has two halves used in turn, so one
-// barrier per reduction suffices: a half is written again only after the
-// barrier of the reduction between).
+// or over the block (kWide true).  A block's warps leave their sums in one of
+// two halves of `red` in turn, so one barrier per reduction suffices: a half
+// is written again only after the barrier of the reduction between.  Every
+// thread then adds all 16 places (the absent warps' hold zeros) in a tree.
+constexpr int kRedFloats = 64;
 template <bool kWide>
 struct RowSum {
-    float* red;
+    float2* red;
     int tpr, half = 0;
-    __device__ RowSum(float* r, int t) : red(r), tpr(t) {}
-    __device__ __forceinline__ float operator()(float v) {
+    __device__ RowSum(float* r, int t) : red(reinterpret_cast<float2*>(r)), tpr(t) {
+        if (kWide) {
+            for (int i = threadIdx.x; i < kRedFloats; i += blockDim.x) r[i] = 0.0f;
+            __syncthreads();
+        }
+    }
+    __device__ __forceinline__ float operator()(float v) { return (*this)(make_float2(v, 0.0f)).x; }
+    // two sums at once
+    __device__ __forceinline__ float2 operator()(float2 v) {
         if constexpr (!kWide) {
-            for (int o = tpr >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+            for (int o = tpr >> 1; o > 0; o >>= 1)
+                v = add2(v, make_float2(__shfl_xor_sync(0xFFFFFFFFu, v.x, o), __shfl_xor_sync(0xFFFFFFFFu, v.y, o)));
             return v;
         } else {
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-            float* s = red + half * 16;
+            for (int o = 16; o > 0; o >>= 1)
+                v = add2(v, make_float2(__shfl_xor_sync(0xFFFFFFFFu, v.x, o), __shfl_xor_sync(0xFFFFFFFFu, v.y, o)));
+            float2* s = red + half * 16;
             half ^= 1;
             if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
             __syncthreads();
-            const int nw = blockDim.x >> 5;
-            v = 0.0f;
-            for (int i = 0; i < nw; ++i) v += s[i];
-            return v;
-        }
-    }
-    // two sums at once
-    __device__ __forceinline__ float2 operator()(float a, float b) {
-        if constexpr (!kWide) {
-            for (int o = tpr >> 1; o > 0; o >>= 1) {
-                a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-                b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
-            }
-            return make_float2(a, b);
-        } else {
+            float2 w[8];
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-                b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+            for (int i = 0; i < 8; ++i) {
+                const float4 q = reinterpret_cast<const float4*>(s)[i];
+                w[i] = add2(make_float2(q.x, q.y), make_float2(q.z, q.w));
             }
-            float2* s = reinterpret_cast<float2*>(red + 32) + half * 16;
-            half ^= 1;
-            if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = make_float2(a, b);
-            __syncthreads();
-            const int nw = blockDim.x >> 5;
-            a = b = 0.0f;
-            for (int i = 0; i < nw; ++i) a += s[i].x, b += s[i].y;
-            return make_float2(a, b);
+#pragma unroll
+            for (int n = 4; n > 0; n >>= 1)
+#pragma unroll
+                for (int i = 0; i < n; ++i) w[i] = add2(w[i], w[i + n]);
+            return w[0];
         }
     }
 };
-constexpr int kRedFloats = 32 + 64;
+
+// Rows come through a ring of shared-memory stages.  Every thread copies
+// (cp.async) and reads its own 16-byte slots only, stages - 1 turns ahead:
+// loads in flight cost no registers, and no barrier guards the ring.  Slots
+// that are never filled (columns behind the row's last) hold zeros.
+template <int kSlots, int V>
+struct Ring {
+    uint32_t base;
+    int slot_stride, stage_bytes;
+    __device__ Ring(const void* smem) {
+        base = smem_u32(smem) + threadIdx.x * 16;
+        slot_stride = blockDim.x * 16;
+        stage_bytes = bytes(blockDim.x);
+    }
+    __device__ void clear(int stages) const {
+        for (int i = 0; i < stages * kSlots * V; ++i) st_shared_v4(base + i * slot_stride, make_uint4(0, 0, 0, 0));
+    }
+    __host__ __device__ static constexpr int bytes(int threads) { return kSlots * V * threads * 16; }
+    __device__ __forceinline__ uint32_t at(int stage, int v, int k) const {
+        return base + stage * stage_bytes + (v * kSlots + k) * slot_stride;
+    }
+    // slots k.. of a vector, or zeros
+    __device__ __forceinline__ F8 get(int stage, int v, int k, bool there, __nv_bfloat16) const {
+        return there ? widen(ld_shared_v4(at(stage, v, k))) : zero8();
+    }
+    __device__ __forceinline__ F8 get(int stage, int v, int k, bool there, float) const {
+        if (!there) return zero8();
+        Raw8<float> w;
+        w.a = ld_shared_v4(at(stage, v, k));
+        w.b = ld_shared_v4(at(stage, v, k + 1));
+        return widen(w);
+    }
+};
+template <typename T>
+__device__ __forceinline__ void ring_copy(uint32_t dst, int slot_stride, const T* src) {
+    cp_async16(dst, src);
+    if constexpr (sizeof(T) == 4) cp_async16(dst + slot_stride, src + 4);
+}
 
 // Mean and 1/deviation of a row held as V vectors of eight (`ok[v]`: this
-// thread has a vector v; absent ones hold zeros).
+// thread has a vector v); leaves x - mean in x.
 template <int V, bool kWide>
-__device__ __forceinline__ float2 row_stats(const float (&x)[V][8], const bool (&ok)[V], int kind, float eps,
-                                            float inv_d, RowSum<kWide>& sum) {
+__device__ __forceinline__ float2 center(F8 (&x)[V], const bool (&ok)[V], int kind, float eps, float inv_d,
+                                         RowSum<kWide>& sum) {
     float mean = 0.0f;
     if (kind == FT_NORM_NONE) return make_float2(0.0f, 1.0f);
     if (kind == FT_NORM_LAYER) {
-        float s = 0.0f;
+        float2 s = both(0.0f);
 #pragma unroll
-        for (int v = 0; v < V; ++v)
+        for (int v = 0; v < V; ++v) s = gather(s, x[v]);  // absent vectors are zeros
+        mean = sum(s.x + s.y) * inv_d;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s += x[v][i];
-        mean = sum(s) * inv_d;
+        for (int v = 0; v < V; ++v) x[v] = add(x[v], -mean);
     }
-    float q = 0.0f;
+    float2 q = both(0.0f);
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-        if (ok[v])
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float c = x[v][i] - mean;
-                q = fmaf(c, c, q);
-            }
-    return make_float2(mean, 1.0f / sqrtf(fmaf(sum(q), inv_d, eps)));
+    for (int v = 0; v < V; ++v) {
+        const float2 more = gather(q, x[v], x[v]);
+        q = ok[v] ? more : q;
+    }
+    return make_float2(mean, 1.0f / sqrtf(fmaf(sum(q.x + q.y), inv_d, eps)));
 }
 
-template <typename XT, int V, bool kWide>
-__global__ void __launch_bounds__(512) k_gated_norm_fwd(const __grid_constant__ FwdParams p) {
-    __shared__ float red[kRedFloats];
+constexpr int kFwdStages = 2;
+template <typename XT>
+constexpr int kFwdSlots = sizeof(XT) / 2 + 1;  // x, y
+
+// kMod: the modulated residual boundary -- y, gate, scale and shift given, no
+// weights, no post norm -- with these facts known to the compiler: what a row
+// spends on asking for each part is then a third of its instructions less.
+template <typename XT, int V, bool kWide, bool k32, bool kMod>
+__global__ void __launch_bounds__(256) k_gated_norm_fwd(const __grid_constant__ FwdParams p) {
+    constexpr int kY = sizeof(XT) / 2;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ __align__(16) float red[kRedFloats];
     const int tpr = kWide ? blockDim.x : p.tpr;
     const int group = kWide ? 0 : threadIdx.x / tpr, groups = kWide ? 1 : blockDim.x / tpr;
     const int t = kWide ? threadIdx.x : threadIdx.x % tpr;
     RowSum<kWide> sum(red, tpr);
-    int col[V];
+    const Ring<kFwdSlots<XT>, V> ring(smem);
+    int col[V], at[V];  // at: where a parameter is read; in range for absent vectors too
     bool ok[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         col[v] = 8 * (t + v * tpr);
         ok[v] = col[v] < p.D;
+        at[v] = ok[v] ? col[v] : 0;
     }
+    ring.clear(kFwdStages);
+    const bool has_y = kMod || p.y, has_gate = kMod || p.gate, has_scale = kMod || p.scale, has_shift = kMod || p.shift;
+    const bool has_w = !kMod && p.w, has_bias = !kMod && p.bias, has_wp = !kMod && p.w_post;
+    const bool has_post = !kMod && p.post != FT_NORM_NONE, has_pre = kMod || p.pre != FT_NORM_NONE;
+    grid_dep_launch();
     grid_dep_wait();
-    const XT* x = static_cast<const XT*>(p.x);
-    Raw8<XT> nx[V];
-    Raw8<__nv_bfloat16> ny[V];
-    auto fetch = [&](int row) {
+    const int step = gridDim.x * groups;
+    auto fetch = [&](int row, int stage) {
+        if (row < p.M) {
+            const XT* x = static_cast<const XT*>(p.x) + (int64_t)row * p.ldx;
+            const __nv_bfloat16* y = p.y + (int64_t)row * p.ldy;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            nx[v] = {};
-            ny[v] = {};
-            if (ok[v] && row < p.M) {
-                load8(nx[v], x + (int64_t)row * p.ldx + col[v]);
-                if (p.y) load8(ny[v], p.y + (int64_t)row * p.ldy + col[v]);
-            }
+            for (int v = 0; v < V; ++v)
+                if (ok[v]) {
+                    ring_copy(ring.at(stage, v, 0), ring.slot_stride, x + col[v]);
+                    if (has_y) ring_copy(ring.at(stage, v, kY), ring.slot_stride, y + col[v]);
+                }
         }
+        cp_async_commit();
     };
-    float amax = 0.0f;
-    fetch(blockIdx.x * groups + group);
+    uint32_t amax = 0;
+    fetch(blockIdx.x * groups + group, 0);
+    int stage = 0;
     // every thread of a block takes the same number of turns: the reductions
     // are the whole warp's or block's
-    for (int first = blockIdx.x * groups; first < p.M; first += gridDim.x * groups) {
+    for (int first = blockIdx.x * groups; first < p.M; first += step, stage ^= 1) {
         const int row = first + group;
         const int b = row < p.M ? sample_of(row, p.offsets, p.B, p.S) : -1;
-        float xv[V][8], u[V][8];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            unpack8(nx[v], xv[v]);
-            unpack8(ny[v], u[v]);
-        }
-        fetch(row + gridDim.x * groups);
+        fetch(row + step, stage ^ 1);
+        cp_async_wait<1>();
         if (kWide && b < 0) continue;  // uniform over the block
-        const int64_t sample = b < 0 ? 0 : b;
+        const bool live = kWide || b >= 0;
+        const int64_t sample = live ? b : 0;
         float2 post = make_float2(0.0f, 1.0f);
-        if (p.y) {
-            post = row_stats<V, kWide>(u, ok, p.post, p.eps_post, p.inv_d, sum);
+        F8 f[V];
+        if (has_y) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) f[v] = ring.get(stage, v, kY, live, __nv_bfloat16());
+            if (has_post) post = center<V, kWide>(f, ok, p.post, p.eps_post, p.inv_d, sum);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                if (!ok[v]) continue;
-                if (p.post != FT_NORM_NONE) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) u[v][i] = (u[v][i] - post.x) * post.y;
-                }
-                float c[8];
-                if (p.w_post) {
-                    load_param8(p.w_post, col[v], p.p32, c);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) u[v][i] *= c[i];
-                }
-                if (p.gate) {
-                    load_param8(p.gate, sample * p.ld_gate + col[v], p.p32, c);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) u[v][i] *= c[i];
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) xv[v][i] = fmaf(p.alpha, u[v][i], xv[v][i]);
-                if (b >= 0) {
-                    store8(static_cast<XT*>(p.r) + (int64_t)row * p.ldr + col[v], xv[v]);
-                }
+                if (has_post) f[v] = mul(f[v], post.y);
+                if (has_wp) f[v] = mul(f[v], load_param8<k32>(p.w_post, at[v]));
+                if (has_gate) f[v] = mul(f[v], load_param8<k32>(p.gate, sample * p.ld_gate + at[v]));
+                f[v] = fma(f[v], p.alpha, ring.get(stage, v, 0, live, XT()));
+                Raw8<XT> r;
+                round8(r, f[v]);
+                if (live && ok[v]) put8(static_cast<XT*>(p.r) + (int64_t)row * p.ldr + col[v], r);
+                f[v] = widen(r);  // the norm reads the stream as it is stored
+                if (!ok[v]) f[v] = zero8();
             }
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) f[v] = ring.get(stage, v, 0, live, XT());
         }
-        const float2 pre = row_stats<V, kWide>(xv, ok, p.pre, p.eps_pre, p.inv_d, sum);
-        if (b < 0) continue;
-        if (p.pre != FT_NORM_NONE) {
+        const float2 pre = center<V, kWide>(f, ok, p.pre, p.eps_pre, p.inv_d, sum);
+        if (!live) continue;
+        if (has_pre) {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                if (!ok[v]) continue;
-                float c[8], f[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] = (xv[v][i] - pre.x) * pre.y;
-                if (p.w) {
-                    load_param8(p.w, col[v], p.p32, c);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) f[i] *= c[i];
+                if (kMod) {
+                    // f rstd (1 + scale) + shift, the scale's part first
+                    const F8 c = load_param8<k32>(p.scale, sample * p.ld_scale + at[v]);
+                    const F8 a = add(mul(c, pre.y), pre.y);
+                    f[v] = fma(f[v], a, load_param8<k32>(p.shift, sample * p.ld_shift + at[v]));
+                } else {
+                    f[v] = mul(f[v], pre.y);
+                    if (has_w) f[v] = mul(f[v], load_param8<k32>(p.w, at[v]));
+                    if (has_bias) f[v] = add(f[v], load_param8<k32>(p.bias, at[v]));
+                    if (has_scale) f[v] = fma(f[v], load_param8<k32>(p.scale, sample * p.ld_scale + at[v]), f[v]);
+                    if (has_shift) f[v] = add(f[v], load_param8<k32>(p.shift, sample * p.ld_shift + at[v]));
                 }
-                if (p.bias) {
-                    load_param8(p.bias, col[v], p.p32, c);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) f[i] += c[i];
-                }
-                if (p.scale) {
-                    load_param8(p.scale, sample * p.ld_scale + col[v], p.p32, c);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) f[i] *= 1.0f + c[i];
-                }
-                if (p.shift) {
-                    load_param8(p.shift, sample * p.ld_shift + col[v], p.p32, c);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) f[i] += c[i];
-                }
-                store8(p.h + (int64_t)row * p.ldh + col[v], f);
-                amax = max_abs8(f, amax);
+                if (ok[v]) amax = store8_max(p.h + (int64_t)row * p.ldh + col[v], f[v], amax);
             }
         }
         if (p.stats && t == 0) p.stats[row] = make_float4(pre.x, pre.y, post.x, post.y);
     }
-    raise_amax(p.amax, amax, red);
+    cp_async_wait<0>();
+    raise_amax(p.amax, amax_of(amax), red);
 }
 
-// Backward.  A block takes `chunk` consecutive rows (its groups one each in
+// Backward.  A block takes `chunk` consecutive rows (its groups one each per
 // turn) and keeps its columns' sums of the current sample in registers; at a
 // sample's last row in the chunk they go to the partial row chunk + sample --
 // a number that no other (chunk, sample) pair met by these ascending steps
 // has, since every step raises one of the two.
-template <typename XT, int V, bool kWide, bool kAcc>
-__global__ void __launch_bounds__(512) k_gated_norm_bwd(const __grid_constant__ BwdParams p) {
-    __shared__ float red[kRedFloats];
-    __shared__ float flush_buf[kWide || !kAcc ? 1 : 256 * 8];
+template <typename XT>
+constexpr int kBwdSlots = 2 + 2 * (sizeof(XT) / 2);  // dh, y, dr, r
+constexpr int kBwdStages = 2;
+template <int V, bool kWide, bool kMod>
+constexpr int kBwdRegs = V == 2 ? 96 : kWide ? (kMod ? 80 : 56) : 128;
+
+// kMod: dh, dr, r, y, gate and scale given, dx and dy wanted, no weights, no
+// post norm; as in the forward.
+template <typename XT, int V, bool kWide, bool k32, bool kMod>
+__global__ void __maxnreg__((kBwdRegs<V, kWide, kMod>)) k_gated_norm_bwd(const __grid_constant__ BwdParams p) {
+    constexpr int kStages = kBwdStages, kDr = 2, kR = 2 + sizeof(XT) / 2;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ __align__(16) float red[kRedFloats];
+    __shared__ __align__(16) float flush_buf[kWide ? 1 : 256 * 8];
     const int tpr = kWide ? blockDim.x : p.tpr;
     const int group = kWide ? 0 : threadIdx.x / tpr, groups = kWide ? 1 : blockDim.x / tpr;
     const int t = kWide ? threadIdx.x : threadIdx.x % tpr;
     RowSum<kWide> sum(red, tpr);
-    int col[V];
+    const Ring<kBwdSlots<XT>, V> ring(smem);
+    int col[V], pat[V];  // pat: where a parameter is read; in range for absent vectors too
     bool ok[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         col[v] = 8 * (t + v * tpr);
         ok[v] = col[v] < p.D;
+        pat[v] = ok[v] ? col[v] : 0;
     }
+    ring.clear(kStages);
+    const bool has_dh = kMod || p.dh, has_dr = kMod || p.dr, has_r = kMod || p.r, has_y = kMod || p.y;
+    const bool has_gate = kMod || p.gate, has_scale = kMod || p.scale, has_w = !kMod && p.w, has_wp = !kMod && p.w_post;
+    const bool pre = kMod || p.pre != FT_NORM_NONE, post = !kMod && p.post != FT_NORM_NONE;
+    const bool want_dx = kMod || p.dx, want_dy = kMod || p.dy, through = want_dy && post;
     const int begin = blockIdx.x * p.chunk, end = min(p.M, begin + p.chunk);
+    const int turns = (end - begin + groups - 1) / groups;
+    grid_dep_launch();
     grid_dep_wait();
-    Raw8<__nv_bfloat16> ndh[V], ny[V];
-    Raw8<XT> ndr[V], nr[V];
-    float4 nst = make_float4(0.0f, 1.0f, 0.0f, 1.0f);
-    auto fetch = [&](int row) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            ndh[v] = {};
-            ny[v] = {};
-            ndr[v] = {};
-            nr[v] = {};
-            if (ok[v] && row < end) {
-                if (p.dh) load8(ndh[v], p.dh + (int64_t)row * p.lddh + col[v]);
-                if (p.dr) load8(ndr[v], static_cast<const XT*>(p.dr) + (int64_t)row * p.lddr + col[v]);
-                if (p.r) load8(nr[v], static_cast<const XT*>(p.r) + (int64_t)row * p.ldr + col[v]);
-                if (p.y) load8(ny[v], p.y + (int64_t)row * p.ldy + col[v]);
-            }
-        }
-        if (p.stats && row < end) nst = __ldg(p.stats + row);
-    };
-    float acc[kAcc ? 3 : 1][V][8];
-#pragma unroll
-    for (int k = 0; k < (kAcc ? 3 : 1); ++k)
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) acc[k][v][i] = 0.0f;
-    float amax = 0.0f;
-    // writes the sums of sample b over the block and clears them
-    auto flush = [&](int b) {
-        if constexpr (kAcc) {
-            float* out = p.partial + ((int64_t)blockIdx.x + b) * 3 * p.D;
-#pragma unroll
-            for (int k = 0; k < 3; ++k) {
-                const bool wanted = k < 2 ? p.need_s : p.need_t;
-                if (!wanted) continue;  // uniform
-                if constexpr (kWide) {
-#pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        if (ok[v]) store8(out + (int64_t)k * p.D + col[v], acc[k][v]);
-                } else {
-                    __syncthreads();
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) flush_buf[threadIdx.x * 8 + i] = acc[k][0][i];
-                    __syncthreads();
-                    for (int c = threadIdx.x; c < p.D; c += blockDim.x) {
-                        float s = 0.0f;
-                        for (int g = 0; g < groups; ++g) s += flush_buf[g * tpr * 8 + c];
-                        out[(int64_t)k * p.D + c] = s;
-                    }
-                }
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) acc[k][v][i] = 0.0f;
-            }
-        }
-    };
-    fetch(begin + group);
-    int row0 = begin;
-    while (row0 < end) {
-        // the run of rows of one sample that starts at row0
-        const int b = sample_of(row0, p.offsets, p.B, p.S);
-        if (b < 0) break;  // behind the last sample: the rest is too
-        const int stop = min(end, max(row0 + 1, p.offsets ? __ldg(p.offsets + b + 1) : (b + 1) * p.S));
-        const int64_t sample = b;
-        for (int first = row0; first < stop; first += groups) {
-            const int row = first + group;
-            const bool live = row < stop;
-            float xh[V][8], yh[V][8], d[V][8], dh[V][8];
-            const float4 st = nst;
+    auto fetch = [&](int turn, int stage) {
+        const int row = begin + turn * groups + group;
+        if (row < end) {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                unpack8(ndh[v], dh[v]);
-                unpack8(ndr[v], d[v]);
-                unpack8(nr[v], xh[v]);
-                unpack8(ny[v], yh[v]);
-                if (!kWide && !live) {  // the row belongs to the next run: no part of the sums
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) dh[v][i] = d[v][i] = xh[v][i] = yh[v][i] = 0.0f;
-                }
-            }
-            // the next row of this run, or the first of the next run
-            fetch(first + groups < stop ? row + groups : stop + group);
-            if (p.pre != FT_NORM_NONE) {
-                float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    if (!ok[v]) continue;
-                    float c[8], z[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        xh[v][i] = (xh[v][i] - st.x) * st.y;
-                        z[i] = dh[v][i];
-                    }
-                    if constexpr (kAcc) {
-                        if (live)
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                acc[0][v][i] += dh[v][i];
-                                acc[1][v][i] = fmaf(dh[v][i], xh[v][i], acc[1][v][i]);
-                            }
-                    }
-                    if (p.scale) {
-                        load_param8(p.scale, sample * p.ld_scale + col[v], p.p32, c);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) z[i] *= 1.0f + c[i];
-                    }
-                    if (p.w) {
-                        load_param8(p.w, col[v], p.p32, c);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) z[i] *= c[i];
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        s0 += z[i];
-                        s1 = fmaf(z[i], xh[v][i], s1);
-                        dh[v][i] = z[i];
-                    }
-                }
-                const float2 m = sum(s0, s1);
-                const float m0 = p.pre == FT_NORM_LAYER ? m.x * p.inv_d : 0.0f, m1 = m.y * p.inv_d;
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        d[v][i] = fmaf(st.y, dh[v][i] - fmaf(xh[v][i], m1, m0), d[v][i]);
-            }
-            if (p.y || p.dy) {
-                float s0 = 0.0f, s1 = 0.0f;
-                float e[V][8];
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    if (!ok[v]) continue;
-                    float c[8];
-                    if (p.post != FT_NORM_NONE) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) yh[v][i] = (yh[v][i] - st.z) * st.w;
-                    }
-                    if constexpr (kAcc) {
-                        if (live)
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) acc[2][v][i] = fmaf(d[v][i], yh[v][i], acc[2][v][i]);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) e[v][i] = p.alpha * d[v][i];
-                    if (p.gate) {
-                        load_param8(p.gate, sample * p.ld_gate + col[v], p.p32, c);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) e[v][i] *= c[i];
-                    }
-                    if (p.w_post) {
-                        load_param8(p.w_post, col[v], p.p32, c);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) e[v][i] *= c[i];
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        s0 += e[v][i];
-                        s1 = fmaf(e[v][i], yh[v][i], s1);
-                    }
-                }
-                if (p.dy && p.post != FT_NORM_NONE) {
-                    const float2 m = sum(s0, s1);
-                    const float m0 = p.post == FT_NORM_LAYER ? m.x * p.inv_d : 0.0f, m1 = m.y * p.inv_d;
-#pragma unroll
-                    for (int v = 0; v < V; ++v)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) e[v][i] = st.w * (e[v][i] - fmaf(yh[v][i], m1, m0));
-                }
-                if (p.dy && live) {
-#pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        if (ok[v]) {
-                            store8(p.dy + (int64_t)row * p.lddy + col[v], e[v]);
-                            amax = max_abs8(e[v], amax);
-                        }
-                }
-            }
-            if (p.dx && live) {
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    if (ok[v]) store8(static_cast<XT*>(p.dx) + (int64_t)row * p.lddx + col[v], d[v]);
+                if (!ok[v]) continue;
+                if (has_dh) ring_copy(ring.at(stage, v, 0), 0, p.dh + (int64_t)row * p.lddh + col[v]);
+                if (has_y) ring_copy(ring.at(stage, v, 1), 0, p.y + (int64_t)row * p.ldy + col[v]);
+                if (has_dr)
+                    ring_copy(ring.at(stage, v, kDr), ring.slot_stride,
+                              static_cast<const XT*>(p.dr) + (int64_t)row * p.lddr + col[v]);
+                if (has_r)
+                    ring_copy(ring.at(stage, v, kR), ring.slot_stride,
+                              static_cast<const XT*>(p.r) + (int64_t)row * p.ldr + col[v]);
             }
         }
-        flush(b);
-        row0 = stop;
+        cp_async_commit();
+    };
+    float4 nst = make_float4(0.0f, 1.0f, 0.0f, 1.0f);
+    auto fetch_stats = [&](int turn) {
+        const int row = begin + turn * groups + group;
+        if ((kMod || p.stats) && row < end) nst = __ldg(p.stats + row);
+    };
+    F8 acc[3][V];
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[k][v] = zero8();
+    uint32_t amax = 0;
+    // writes the sums of sample b over the block and clears them
+    auto flush = [&](int b) {
+        float* out = p.partial + ((int64_t)blockIdx.x + b) * 3 * p.D;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            const bool wanted = k < 2 ? p.need_s : p.need_t;
+            if (!wanted) continue;  // uniform
+            if constexpr (kWide) {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    if (ok[v]) {
+                        Raw8<float> w;
+                        round8(w, acc[k][v]);
+                        put8(out + (int64_t)k * p.D + col[v], w);
+                    }
+            } else {
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<float2*>(flush_buf + threadIdx.x * 8 + 2 * i) = acc[k][0].p[i];
+                __syncthreads();
+                for (int c = threadIdx.x; c < p.D; c += blockDim.x) {
+                    float s = 0.0f;
+                    for (int g = 0; g < groups; ++g) s += flush_buf[g * tpr * 8 + c];
+                    out[(int64_t)k * p.D + c] = s;
+                }
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) acc[k][v] = zero8();
+        }
+    };
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) fetch(k, k);
+    fetch_stats(0);
+    int b = 0, stop = begin;  // the current sample, and where its rows (in this chunk) end
+    int stage = 0, ahead = kStages - 1;
+    for (int turn = 0; turn < turns; ++turn) {
+        const int row = begin + turn * groups + group;
+        const int turn_end = min(end, begin + (turn + 1) * groups);
+        const float4 st = nst;
+        fetch_stats(turn + 1);
+        // the stage read in the turn before takes the turn stages - 1 ahead:
+        // only this thread reads its slots
+        fetch(turn + kStages - 1, ahead);
+        cp_async_wait<kStages - 1>();
+        // one pass over the turn's rows for each sample that has some of them
+        int at = begin + turn * groups;
+        while (at < turn_end) {
+            if (at >= stop) {
+                b = sample_of(at, p.offsets, p.B, p.S);
+                if (b < 0) break;
+                stop = min(end, max(at + 1, p.offsets ? __ldg(p.offsets + b + 1) : (b + 1) * p.S));
+            }
+            const int upto = min(stop, turn_end);
+            // rows of other samples and stale slots count as zeros
+            const bool live = kWide || (row >= at && row < upto);
+            const int64_t sample = b;
+            float a0 = 0.0f, a1 = 0.0f;  // d = dr + rstd z + a1 (r - mean) + a0
+            F8 z[V];  // dh (1 + scale) w
+            if (pre) {
+                float2 s0 = both(0.0f), s1 = both(0.0f);
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const F8 xh = mul(add(ring.get(stage, v, kR, live, XT()), live ? -st.x : 0.0f), live ? st.y : 0.0f);
+                    z[v] = ring.get(stage, v, 0, live, __nv_bfloat16());
+                    acc[0][v] = add(acc[0][v], z[v]);
+                    acc[1][v] = fma(z[v], xh, acc[1][v]);
+                    if (has_scale) z[v] = fma(z[v], load_param8<k32>(p.scale, sample * p.ld_scale + pat[v]), z[v]);
+                    if (has_w) z[v] = mul(z[v], load_param8<k32>(p.w, pat[v]));
+                    s0 = gather(s0, z[v]);  // an absent vector's z is zero
+                    s1 = gather(s1, z[v], xh);
+                }
+                const float2 m = sum(make_float2(s0.x + s0.y, s1.x + s1.y));
+                a0 = p.pre == FT_NORM_LAYER && live ? -m.x * p.inv_d * st.y : 0.0f;
+                a1 = live ? -m.y * p.inv_d * st.y * st.y : 0.0f;
+            }
+            auto normed_y = [&](int v) {
+                const F8 y = ring.get(stage, v, 1, live, __nv_bfloat16());
+                return post ? mul(add(y, live ? -st.z : 0.0f), live ? st.w : 0.0f) : y;
+            };
+            float2 s0 = both(0.0f), s1 = both(0.0f);
+            F8 e[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                e[v] = has_dr ? ring.get(stage, v, kDr, live, XT()) : zero8();
+                if (pre) {
+                    // the row is read again rather than kept: registers set how many blocks an SM holds
+                    const F8 xc = add(ring.get(stage, v, kR, live, XT()), live ? -st.x : 0.0f);
+                    e[v] = add(fma(xc, a1, fma(z[v], live ? st.y : 0.0f, e[v])), a0);
+                }
+                F8 yh = zero8();
+                if (has_y) {
+                    yh = normed_y(v);
+                    acc[2][v] = fma(e[v], yh, acc[2][v]);
+                }
+                if (want_dx && live && ok[v]) {
+                    Raw8<XT> w;
+                    round8(w, e[v]);
+                    put8(static_cast<XT*>(p.dx) + (int64_t)row * p.lddx + col[v], w);
+                }
+                if (want_dy) {
+                    if (has_gate) {
+                        e[v] = mul(e[v], mul(load_param8<k32>(p.gate, sample * p.ld_gate + pat[v]), p.alpha));
+                    } else {
+                        e[v] = mul(e[v], p.alpha);
+                    }
+                    if (has_wp) e[v] = mul(e[v], load_param8<k32>(p.w_post, pat[v]));
+                    if (through) {
+                        if (!ok[v]) e[v] = zero8();
+                        s0 = gather(s0, e[v]);
+                        s1 = gather(s1, e[v], yh);
+                    } else if (live && ok[v]) {
+                        amax = store8_max(p.dy + (int64_t)row * p.lddy + col[v], e[v], amax);
+                    }
+                }
+            }
+            if (through) {
+                const float2 m = sum(make_float2(s0.x + s0.y, s1.x + s1.y));
+                const float e0 = p.post == FT_NORM_LAYER ? m.x * p.inv_d : 0.0f, e1 = m.y * p.inv_d;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    if (!ok[v] || !live) continue;
+                    amax = store8_max(p.dy + (int64_t)row * p.lddy + col[v],
+                                      mul(add(fma(normed_y(v), -e1, e[v]), -e0), st.w), amax);
+                }
+            }
+            if (stop <= turn_end) flush(b);
+            at = upto;
+        }
+        if (b < 0) break;  // behind the last sample: the rest is too
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+        ahead = ahead + 1 == kStages ? 0 : ahead + 1;
     }
-    raise_amax(p.amax, amax, red);
+    cp_async_wait<0>();
+    raise_amax(p.amax, amax_of(amax), red);
 }
 
 struct ReduceParams {
-    int M, D, B, S, chunk, chunks;
+    int M, D, B, S, chunk;
     const int32_t* offsets;
     float alpha;
     bool p32;
     int64_t ld_gate, ld_scale;
     const void *gate, *scale, *w_post, *w, *bias;
-    const float* partial;
+    const float* partial;  // [chunks + B][3][D]
+    float* sums;           // [B][3][D] for the weights' gradients, or null
     float *dgate, *dscale, *dshift, *dw_post, *dw, *dbias;
     bool need_s, need_t;
-    bool all_samples;  // one block row walks every sample (the weights' gradients sum over them)
 };
 
-// Adds the partial rows of each sample, in ascending order: 32 columns per
-// block, kGroups threads per column.  Sample b's partial rows are those of
-// the chunks that hold its rows.
-constexpr int kReduceGroups = 16;
+// Adds the partial rows of each sample in a fixed order: 32 columns per
+// block, a thread per column and every kReduceGroups-th partial row, so that
+// all of a thread's loads are in flight at once.  Sample b's partial rows
+// are those of the chunks that hold its rows.
+constexpr int kReduceGroups = 32;
 __global__ void __launch_bounds__(32 * kReduceGroups) k_gated_norm_reduce(const __grid_constant__ ReduceParams p) {
     __shared__ float part[3][kReduceGroups][33];
     const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
     const bool ok = c < p.D;
+    grid_dep_launch();
     grid_dep_wait();
-    float dw = 0.0f, db = 0.0f, dwp = 0.0f;
     const float w = p.w && ok ? load_param(p.w, c, p.p32) : 1.0f;
     const float bias = p.bias && ok ? load_param(p.bias, c, p.p32) : 0.0f;
     const float wp = p.w_post && ok ? load_param(p.w_post, c, p.p32) : 1.0f;
-    const int step = p.all_samples ? 1 : gridDim.y;
-    for (int b = p.all_samples ? 0 : blockIdx.y; b < p.B; b += step) {
+    for (int b = blockIdx.y; b < p.B; b += gridDim.y) {
         int lo = p.offsets ? __ldg(p.offsets + b) : b * p.S;
         int hi = p.offsets ? __ldg(p.offsets + b + 1) : (b + 1) * p.S;
         lo = max(lo, 0);
@@ -532,8 +550,10 @@ __global__ void __launch_bounds__(32 * kReduceGroups) k_gated_norm_reduce(const 
         float s[3] = {0.0f, 0.0f, 0.0f};
         if (ok && lo < hi) {
             const int c0 = lo / p.chunk, c1 = (hi - 1) / p.chunk;
-            for (int k = c0 + g; k <= c1; k += kReduceGroups) {
-                const float* q = p.partial + ((int64_t)k + b) * 3 * p.D + c;
+            const float* q = p.partial + ((int64_t)c0 + b + g) * 3 * p.D + c;
+            const int64_t step = (int64_t)kReduceGroups * 3 * p.D;
+#pragma unroll 4
+            for (int k = c0 + g; k <= c1; k += kReduceGroups, q += step) {
                 if (p.need_s) {
                     s[0] += __ldg(q);
                     s[1] += __ldg(q + p.D);
@@ -545,30 +565,48 @@ __global__ void __launch_bounds__(32 * kReduceGroups) k_gated_norm_reduce(const 
 #pragma unroll
         for (int k = 0; k < 3; ++k) part[k][g][lane] = s[k];
         __syncthreads();
-        if (g == 0 && ok) {
+        // warp k adds sum k: a column per lane
+        if (g < 3) {
+            float t = 0.0f;
 #pragma unroll
-            for (int k = 0; k < 3; ++k) {
-                s[k] = 0.0f;
-                for (int i = 0; i < kReduceGroups; ++i) s[k] += part[k][i][lane];
-            }
+            for (int i = 0; i < kReduceGroups; ++i) t += part[g][i][lane];
+            part[g][0][lane] = t;
+        }
+        __syncthreads();
+        if (g == 0 && ok) {
+            const float s0 = part[0][0][lane], s1 = part[1][0][lane], s2 = part[2][0][lane];
             const int64_t at = (int64_t)b * p.D + c;
-            if (p.dshift) p.dshift[at] = s[0];
-            if (p.dscale) p.dscale[at] = fmaf(w, s[1], bias * s[0]);
-            if (p.dgate) p.dgate[at] = p.alpha * wp * s[2];
-            if (p.all_samples) {
-                const float a = p.scale ? 1.0f + load_param(p.scale, (int64_t)b * p.ld_scale + c, p.p32) : 1.0f;
-                dw = fmaf(a, s[1], dw);
-                db = fmaf(a, s[0], db);
-                const float gate = p.gate ? load_param(p.gate, (int64_t)b * p.ld_gate + c, p.p32) : 1.0f;
-                dwp = fmaf(p.alpha * gate, s[2], dwp);
+            if (p.dshift) p.dshift[at] = s0;
+            if (p.dscale) p.dscale[at] = fmaf(w, s1, bias * s0);
+            if (p.dgate) p.dgate[at] = p.alpha * wp * s2;
+            if (p.sums) {
+                float* o = p.sums + (int64_t)b * 3 * p.D + c;
+                o[0] = s0;
+                o[p.D] = s1;
+                o[2 * (int64_t)p.D] = s2;
             }
         }
     }
-    if (g == 0 && ok && p.all_samples) {
-        if (p.dw) p.dw[c] = dw;
-        if (p.dbias) p.dbias[c] = db;
-        if (p.dw_post) p.dw_post[c] = dwp;
+}
+
+// The weights' gradients from the samples' sums.
+__global__ void __launch_bounds__(64) k_gated_norm_weights(const __grid_constant__ ReduceParams p) {
+    const int c = blockIdx.x * 64 + threadIdx.x;
+    grid_dep_wait();
+    if (c >= p.D) return;
+    float dw = 0.0f, db = 0.0f, dwp = 0.0f;
+#pragma unroll 4
+    for (int b = 0; b < p.B; ++b) {
+        const float* q = p.sums + (int64_t)b * 3 * p.D + c;
+        const float a = p.scale ? 1.0f + load_param(p.scale, (int64_t)b * p.ld_scale + c, p.p32) : 1.0f;
+        const float gate = p.gate ? load_param(p.gate, (int64_t)b * p.ld_gate + c, p.p32) : 1.0f;
+        db = fmaf(a, q[0], db);
+        dw = fmaf(a, q[p.D], dw);
+        dwp = fmaf(p.alpha * gate, q[2 * (int64_t)p.D], dwp);
     }
+    if (p.dw) p.dw[c] = dw;
+    if (p.dbias) p.dbias[c] = db;
+    if (p.dw_post) p.dw_post[c] = dwp;
 }
 
 }  // namespace norm

@@ -562,8 +562,8 @@ size_t ft_qk_rope_workspace_bytes(int64_t M, int64_t hd);
  *         codes (v), with one FP32 scale per 256 consecutive elements
  *         (m_scale, v_scale [ceil(n / 256)]; NULL with 32-bit states).
  *   weight_decay: this tensor's.
- * Pointers are aligned to their element type; tensors whose pointers are
- * 16-byte aligned (8-byte for codes) take the vector path.                 */
+ * Pointers are aligned to their element type; a tensor all of whose pointers
+ * are aligned to four elements takes the vector path.                      */
 typedef struct {
     float* p;
     void* p16;
