@@ -36,7 +36,7 @@ __all__ = [
     "ft_set_cooperative_quantizer", "ft_set_gemm_mode", "GEMM_PAIRS", "GEMM_SINGLE", "prepare_layer", "svd_split", "Workspace", "timing",
     "GatedNorm", "GatedNormGrads", "NORM_NONE", "NORM_RMS", "NORM_LAYER", "ft_gated_norm_fwd", "ft_gated_norm_bwd",
     "ft_gelu_bwd_bf16", "Rope", "ROPE_PAIRS", "ROPE_HALVES", "rope_freqs", "ft_qk_rope_fwd", "ft_qk_rope_bwd",
-    "AdamW", "ft_adamw_decode",
+    "AdamW", "ft_adamw_decode", "DitBlock", "BlockGrads",
 ]
 
 
@@ -419,3 +419,4 @@ from .blockops import (NORM_LAYER, NORM_NONE, NORM_RMS, ROPE_HALVES, ROPE_PAIRS,
                        GatedNormGrads, Rope, ft_gated_norm_bwd, ft_gated_norm_fwd, ft_gelu_bwd_bf16,
                        ft_qk_rope_bwd, ft_qk_rope_fwd, rope_freqs)
 from .optim import AdamW, ft_adamw_decode  # noqa: E402
+from .block import BlockGrads, DitBlock  # noqa: E402

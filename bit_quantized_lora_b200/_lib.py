@@ -170,19 +170,19 @@ SIGNATURES = {
     "ft_linear_fwd_noalloc": (ctypes.c_int, [ctypes.POINTER(FtLinear), c_vp, c_i64, c_vp, c_vp,
                                              ctypes.c_int, c_vp, c_vp]),
     "ft_linear_fwd_noalloc_max_bytes": (ctypes.c_size_t, []),
-    "ft_gated_norm_fwd": (ctypes.c_int, [ctypes.POINTER(FtGatedNorm), c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp,
+    "ft_gated_norm_fwd": (ctypes.c_int, [c_vp, c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp,
                                          c_i64, c_vp, c_vp, c_vp]),
-    "ft_gated_norm_bwd": (ctypes.c_int, [ctypes.POINTER(FtGatedNorm), c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp,
-                                         c_i64, c_vp, ctypes.POINTER(FtGatedNormGrads), c_vp, ctypes.c_size_t, c_vp]),
+    "ft_gated_norm_bwd": (ctypes.c_int, [c_vp, c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp,
+                                         c_i64, c_vp, c_vp, c_vp, ctypes.c_size_t, c_vp]),
     "ft_gated_norm_workspace_bytes": (ctypes.c_size_t, [c_i64, c_i64, c_i64]),
     "ft_gelu_bwd_bf16": (ctypes.c_int, [c_vp, c_vp, c_vp, c_i64, c_vp, c_vp]),
-    "ft_qk_rope_fwd": (ctypes.c_int, [ctypes.POINTER(FtRope), c_vp, c_i64, ctypes.POINTER(FtHeads),
-                                      ctypes.POINTER(FtHeads), ctypes.POINTER(FtHeads), c_vp]),
-    "ft_qk_rope_bwd": (ctypes.c_int, [ctypes.POINTER(FtRope), ctypes.POINTER(FtHeads), ctypes.POINTER(FtHeads),
-                                      ctypes.POINTER(FtHeads), c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_vp, c_vp,
+    "ft_qk_rope_fwd": (ctypes.c_int, [c_vp, c_vp, c_i64, c_vp,
+                                      c_vp, c_vp, c_vp]),
+    "ft_qk_rope_bwd": (ctypes.c_int, [c_vp, c_vp, c_vp,
+                                      c_vp, c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_vp, c_vp,
                                       ctypes.c_size_t, c_vp]),
     "ft_qk_rope_workspace_bytes": (ctypes.c_size_t, [c_i64, c_i64]),
-    "ft_adamw_step": (ctypes.c_int, [c_vp, c_i64, ctypes.POINTER(FtAdamwHyper), ctypes.c_int, c_vp, c_vp, c_vp,
+    "ft_adamw_step": (ctypes.c_int, [c_vp, c_i64, c_vp, ctypes.c_int, c_vp, c_vp, c_vp,
                                      c_vp]),
     "ft_adamw_decode": (ctypes.c_int, [c_vp, c_vp, c_i64, ctypes.c_int, c_vp, c_vp]),
     "ft_timing_enable": (ctypes.c_int, [ctypes.c_int]),

@@ -10,17 +10,24 @@ stream.  They may be captured in a CUDA graph.
 """
 from __future__ import annotations
 
-import ctypes
 import functools
+import struct
 from dataclasses import dataclass
 
 import torch
 
-from ._lib import FtGatedNorm, FtGatedNormGrads, FtHeads, FtRope, check, load
+from ._lib import check, load
 
 NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2
 ROPE_PAIRS, ROPE_HALVES = 0, 1
-_DTYPE = {torch.bfloat16: 0, torch.float32: 1}
+_BF16, _F32 = torch.bfloat16, torch.float32
+_DTYPE = {_BF16: 0, _F32: 1}
+# the C structs (ft_gated_norm, ft_gated_norm_grads, ft_rope, ft_heads) as bytes: a call fills its own
+_NORM = struct.Struct("@3qP2i3f2i3q6P")
+_NORM_GRADS = struct.Struct("@PqPq7P")
+_ROPE = struct.Struct("@2q4i4i2if2i4P")
+_HEADS = struct.Struct("@P3q")
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _on_device(at: int):
@@ -29,58 +36,57 @@ def _on_device(at: int):
     def wrap(fn):
         @functools.wraps(fn)
         def call(*args, stream=None, **kw):
-            dev = args[at].device
-            if dev.type != "cuda":
+            dev = args[at].get_device()
+            if dev < 0:
                 raise TypeError(f"{fn.__name__} needs CUDA tensors")
-            if stream is None and dev.index == torch.cuda.current_device():
+            if stream is None and dev == torch._C._cuda_getDevice():
                 return fn(*args, **kw)
             stream = torch.cuda.current_stream(dev) if stream is None else stream
-            if stream.device != dev:
-                raise ValueError(f"the stream is on {stream.device}, the tensors are on {dev}")
+            if stream.device.index != dev:
+                raise ValueError(f"the stream is on {stream.device}, the tensors are on cuda:{dev}")
             with torch.cuda.stream(stream):
                 return fn(*args, **kw)
         return call
     return wrap
 
 
-def _raw_stream(t: torch.Tensor) -> int:
-    return torch.cuda.current_stream(t.device).cuda_stream
+def _ptr(t) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+def _same_device(t: torch.Tensor, dev: int, name: str) -> None:
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the call is on cuda:{dev}")
 
 
-def _same_device(t: torch.Tensor, dev, name: str) -> None:
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, the call is on {dev}")
-
-
-def _matrix(t: torch.Tensor, name: str, dtype, rows: int, cols: int, dev) -> int:
+def _matrix(t: torch.Tensor, name: str, dtype, rows: int, cols: int, dev: int) -> int:
     """Checks a row-major matrix and returns its leading dimension."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    _same_device(t, dev, name)
-    if tuple(t.shape) != (rows, cols):
+    if t.get_device() != dev:
+        _same_device(t, dev, name)
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} must be [{rows}, {cols}], not {list(t.shape)}")
-    if t.stride(1) != 1 and cols > 1:
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride")
-    return t.stride(0) if rows > 1 else cols
+    return ld if rows > 1 else cols
 
 
-def _f32(t, name: str, n: int, dev):
+def _f32(t, name: str, n: int, dev: int) -> int:
     if t is None:
-        return None
-    if t.dtype != torch.float32 or t.numel() < n or not t.is_contiguous():
+        return 0
+    if t.dtype is not _F32 or t.numel() < n or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous float32 tensor of {n}")
-    _same_device(t, dev, name)
+    if t.get_device() != dev:
+        _same_device(t, dev, name)
     return t.data_ptr()
 
 
-def _scratch(ws, nbytes: int, dev):
+def _scratch(ws, nbytes: int, like: torch.Tensor):
     """Scratch of one call: the caller's workspace, or memory of the current
     stream (an allocation that a captured graph owns with the call)."""
-    return ws.get(nbytes, dev) if ws is not None else torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    return ws.get(nbytes, like.device) if ws is not None else like.new_empty(nbytes, dtype=torch.uint8)
 
 
 # ---------------------------------------------------------------- gated norm
@@ -113,44 +119,51 @@ class GatedNormGrads:
     dw_post: torch.Tensor | None = None
 
 
-def _norm_view(norm: GatedNorm, M: int, D: int, xt, mods, offsets, dev):
-    """FtGatedNorm of a call, and its number of samples."""
-    rows = {m.shape[0] if m.dim() == 2 else 1 for m in mods if m is not None} - {1}
+def _norm_view(norm: GatedNorm, M: int, D: int, xt, gate, scale, shift, offsets, dev: int):
+    """The C struct of a call, and its number of samples."""
+    if xt not in _DTYPE:
+        raise TypeError(f"the residual stream must be bfloat16 or float32, not {xt}")
+    B, pt = 1, None
+    mods = (("gate", gate), ("scale", scale), ("shift", shift))
     if offsets is not None:
-        if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 2 or not offsets.is_contiguous():
+        if offsets.dtype is not torch.int32 or offsets.dim() != 1 or len(offsets) < 2 or not offsets.is_contiguous():
             raise TypeError("offsets must be a contiguous int32 tensor [samples + 1]")
         _same_device(offsets, dev, "offsets")
-        rows.add(offsets.numel() - 1)
-    rows = rows - {1} if len(rows) > 1 else rows
-    if len(rows) > 1:
-        raise ValueError(f"gate, scale, shift and offsets disagree on the samples: {sorted(rows)}")
-    B = rows.pop() if rows else 1
-    pt, ld = None, []
-    for name, t in zip(("gate", "scale", "shift"), mods):
+        B = len(offsets) - 1
+    else:
+        for _, t in mods:
+            if t is not None and t.dim() == 2 and len(t) != 1:
+                B = len(t)
+                break
+    ld = []
+    for name, t in mods:
         if t is None:
             ld.append(0)
             continue
-        if t.dim() not in (1, 2) or t.shape[-1] != D or (t.dim() == 2 and t.shape[0] not in (1, B)):
-            raise ValueError(f"{name} must be [{B}, {D}] or [{D}], not {list(t.shape)}")
-        if t.stride(-1) != 1:
+        shape, stride = t.shape, t.stride()
+        if shape != (B, D) and shape != (D,) and shape != (1, D):
+            raise ValueError(f"{name} must be [{B}, {D}] or [{D}], not {list(shape)}")
+        if stride[-1] != 1:
             raise ValueError(f"{name} must have unit column stride")
-        ld.append(t.stride(0) if t.dim() == 2 and t.shape[0] > 1 else 0)
+        ld.append(stride[0] if len(shape) == 2 and shape[0] > 1 else 0)
+        pt = _param_type(t, pt, dev)
     for name, t in (("weight", norm.weight), ("bias", norm.bias), ("w_post", norm.w_post)):
-        if t is not None and (tuple(t.shape) != (D,) or not t.is_contiguous()):
-            raise ValueError(f"{name} must be contiguous [{D}], not {list(t.shape)}")
-    for t in (*mods, norm.weight, norm.bias, norm.w_post):
-        if t is None:
-            continue
+        if t is not None:
+            if t.shape != (D,) or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous [{D}], not {list(t.shape)}")
+            pt = _param_type(t, pt, dev)
+    eps = norm.eps
+    return _NORM.pack(M, D, B, _ptr(offsets), norm.pre, norm.post, eps, eps if norm.eps_post is None else norm.eps_post,
+                      norm.alpha, _DTYPE[xt], 0 if pt is _BF16 else 1, *ld, _ptr(gate), _ptr(scale), _ptr(shift),
+                      _ptr(norm.w_post), _ptr(norm.weight), _ptr(norm.bias)), B
+
+
+def _param_type(t: torch.Tensor, pt, dev: int):
+    if t.get_device() != dev:
         _same_device(t, dev, "a parameter vector")
-        if t.dtype not in _DTYPE or (pt is not None and t.dtype != pt):
-            raise TypeError("gate, scale, shift and the norms' weights must all be bfloat16 or all float32")
-        pt = t.dtype
-    if xt not in _DTYPE:
-        raise TypeError(f"the residual stream must be bfloat16 or float32, not {xt}")
-    eps_post = norm.eps if norm.eps_post is None else norm.eps_post
-    return FtGatedNorm(M, D, B, _ptr(offsets), norm.pre, norm.post, norm.eps, eps_post, norm.alpha, _DTYPE[xt],
-                       _DTYPE[pt or torch.float32], *ld, *map(_ptr, mods), _ptr(norm.w_post), _ptr(norm.weight),
-                       _ptr(norm.bias)), B
+    if t.dtype not in _DTYPE or (pt is not None and t.dtype is not pt):
+        raise TypeError("gate, scale, shift and the norms' weights must all be bfloat16 or all float32")
+    return t.dtype
 
 
 @_on_device(1)
@@ -169,28 +182,28 @@ def ft_gated_norm_fwd(norm: GatedNorm, x: torch.Tensor, y: torch.Tensor | None =
     if x.dim() != 2:
         raise ValueError("x must be [rows, channels]")
     M, D = x.shape
-    dev = x.device
-    n, _ = _norm_view(norm, M, D, x.dtype, (gate, scale, shift), offsets, dev)
-    ldx = _matrix(x, "x", x.dtype, M, D, dev)
+    dev, xt = x.get_device(), x.dtype
+    n, _ = _norm_view(norm, M, D, xt, gate, scale, shift, offsets, dev)
+    ldx = _matrix(x, "x", xt, M, D, dev)
     ldy = ldr = ldh = 0
     if y is not None:
-        ldy = _matrix(y, "y", torch.bfloat16, M, D, dev)
-        r = torch.empty(M, D, dtype=x.dtype, device=dev) if r is None else r
-        ldr = _matrix(r, "r", x.dtype, M, D, dev)
+        ldy = _matrix(y, "y", _BF16, M, D, dev)
+        r = x.new_empty((M, D)) if r is None else r
+        ldr = _matrix(r, "r", xt, M, D, dev)
     elif r is not None:
         raise ValueError("r is written only with y")
     if norm.pre != NORM_NONE:
-        h = torch.empty(M, D, dtype=torch.bfloat16, device=dev) if h is None else h
-        ldh = _matrix(h, "h", torch.bfloat16, M, D, dev)
+        h = x.new_empty((M, D), dtype=_BF16) if h is None else h
+        ldh = _matrix(h, "h", _BF16, M, D, dev)
     elif h is not None:
         raise ValueError("h is written only with a pre norm")
     if stats is True:
-        stats = torch.empty(M, 4, dtype=torch.float32, device=dev)
+        stats = x.new_empty((M, 4), dtype=_F32)
     elif stats is False:
         stats = None
     check("ft_gated_norm_fwd", load().ft_gated_norm_fwd(
-        ctypes.byref(n), x.data_ptr(), ldx, _ptr(y), ldy, _ptr(r), ldr, _ptr(h), ldh,
-        _f32(stats, "stats", 4 * M, dev), _f32(amax_h, "amax_h", 1, dev), _raw_stream(x)))
+        n, x.data_ptr(), ldx, _ptr(y), ldy, _ptr(r), ldr, _ptr(h), ldh, _f32(stats, "stats", 4 * M, dev),
+        _f32(amax_h, "amax_h", 1, dev), _raw_stream(dev)))
     return (x if y is None else r), h, stats
 
 
@@ -226,46 +239,57 @@ def _gated_norm_bwd(some, norm, dh, r, stats, dr, y, gate, scale, shift, offsets
     if some.dim() != 2:
         raise ValueError("gradients must be [rows, channels]")
     M, D = some.shape
-    dev = some.device
-    xt = r.dtype if r is not None else dr.dtype if dr is not None else dx.dtype if dx is not None else torch.bfloat16
-    n, B = _norm_view(norm, M, D, xt, (gate, scale, shift), offsets, dev)
-    given = dict(gate=gate, scale=scale, shift=shift, weight=norm.weight, bias=norm.bias, w_post=norm.w_post)
+    dev = some.get_device()
+    xt = r.dtype if r is not None else dr.dtype if dr is not None else dx.dtype if dx is not None else _BF16
+    n, B = _norm_view(norm, M, D, xt, gate, scale, shift, offsets, dev)
+    weight, bias, w_post = norm.weight, norm.bias, norm.w_post
+    given = (gate, scale, shift, weight, bias, w_post)
     if param_grads is True:
-        wanted = {k for k, v in given.items() if v is not None}
+        wanted = [v is not None for v in given]
     else:
-        wanted = set(param_grads or ())
-        unknown = {k for k in wanted if k not in _PARAMS or given[k] is None}
+        names = set(param_grads or ())
+        wanted = [k in names for k in _PARAMS]
+        unknown = names.difference(k for k, v in zip(_PARAMS, given) if v is not None)
         if unknown:
             raise ValueError(f"no gradient for {sorted(unknown)}: not among the parameters given")
     if residual is None:
         residual = y is not None or gate is not None or dy is not None or norm.post != NORM_NONE
-    if y is None and (norm.post != NORM_NONE or wanted & {"gate", "w_post"}):
+    if y is None and (norm.post != NORM_NONE or wanted[0] or wanted[5]):
         raise ValueError("the post norm and the gradient of the gate need y")
-    lds = {}
-    for name, t, dtype in (("dh", dh, torch.bfloat16), ("dr", dr, xt), ("r", r, xt), ("y", y, torch.bfloat16)):
-        lds[name] = 0 if t is None else _matrix(t, name, dtype, M, D, dev)
-    if need_dx and dx is None:
-        dx = torch.empty(M, D, dtype=xt, device=dev)
+    lddh = 0 if dh is None else _matrix(dh, "dh", _BF16, M, D, dev)
+    lddr = 0 if dr is None else _matrix(dr, "dr", xt, M, D, dev)
+    ldr = 0 if r is None else _matrix(r, "r", xt, M, D, dev)
+    ldy = 0 if y is None else _matrix(y, "y", _BF16, M, D, dev)
     if not need_dx:
         dx = None
+    elif dx is None:
+        dx = some.new_empty((M, D), dtype=xt)
     if residual and dy is None:
-        dy = torch.empty(M, D, dtype=torch.bfloat16, device=dev)
+        dy = some.new_empty((M, D), dtype=_BF16)
     lddx = 0 if dx is None else _matrix(dx, "dx", xt, M, D, dev)
-    lddy = 0 if dy is None else _matrix(dy, "dy", torch.bfloat16, M, D, dev)
-    out = {k: torch.empty((B, D) if k in ("gate", "scale", "shift") else (D,), dtype=torch.float32, device=dev)
-           for k in _PARAMS if k in wanted}
-    nws = load().ft_gated_norm_workspace_bytes(M, D, B) if wanted else 0
-    buf = _scratch(ws, nws, dev) if nws else None
-    g = FtGatedNormGrads(_ptr(dx), lddx, _ptr(dy), lddy, *(_ptr(out.get(k)) for k in ("gate", "scale", "shift")),
-                         *(_ptr(out.get(k)) for k in ("w_post", "weight", "bias")), _f32(amax_dy, "amax_dy", 1, dev))
+    lddy = 0 if dy is None else _matrix(dy, "dy", _BF16, M, D, dev)
+    # the gradients of modulation vectors share one allocation, those of weights another
+    out, buf, nws = [None] * 6, None, 0
+    mods, weights = sum(wanted[:3]), sum(wanted[3:])
+    if mods:
+        parts = iter(some.new_empty((mods, B, D), dtype=_F32).unbind(0))
+        out[:3] = [next(parts) if w else None for w in wanted[:3]]
+    if weights:
+        parts = iter(some.new_empty((weights, D), dtype=_F32).unbind(0))
+        out[3:] = [next(parts) if w else None for w in wanted[3:]]
+    if mods or weights:
+        nws = load().ft_gated_norm_workspace_bytes(M, D, B)
+        buf = _scratch(ws, nws, some)
+    dgate, dscale, dshift, dw, db, dwp = out
+    g = _NORM_GRADS.pack(_ptr(dx), lddx, _ptr(dy), lddy, _ptr(dgate), _ptr(dscale), _ptr(dshift), _ptr(dwp), _ptr(dw),
+                         _ptr(db), _f32(amax_dy, "amax_dy", 1, dev))
     check("ft_gated_norm_bwd", load().ft_gated_norm_bwd(
-        ctypes.byref(n), _ptr(dh), lds["dh"], _ptr(dr), lds["dr"], _ptr(r), lds["r"], _ptr(y), lds["y"],
-        _f32(stats, "stats", 4 * M, dev), ctypes.byref(g), _ptr(buf), 0 if buf is None else buf.numel(),
-        _raw_stream(some)))
-    for k in ("gate", "scale", "shift"):
-        if k in out and tuple(given[k].shape) != (B, D):
-            out[k] = out[k].sum(0).view(given[k].shape)
-    return GatedNormGrads(dx, dy, **{("dw_post" if k == "w_post" else "d" + k): v for k, v in out.items()})
+        n, _ptr(dh), lddh, _ptr(dr), lddr, _ptr(r), ldr, _ptr(y), ldy, _f32(stats, "stats", 4 * M, dev), g,
+        _ptr(buf), nws, _raw_stream(dev)))
+    for i in range(3):
+        if wanted[i] and given[i].shape != (B, D):  # one for all samples
+            out[i] = (out[i].sum(0) if B > 1 else out[i]).view(given[i].shape)
+    return GatedNormGrads(dx, dy, *out)
 
 
 # ---------------------------------------------------------------- GELU backward
@@ -275,15 +299,16 @@ def ft_gelu_bwd_bf16(y: torch.Tensor, dh: torch.Tensor, out: torch.Tensor | None
     """dy = dh GELU'(y) on bf16, the backward of ft_gelu_bf16.  amax_dy: an
     optional float32 device scalar (>= 0) raised to max|dy|."""
     out = torch.empty_like(y) if out is None else out
+    dev, shape = y.get_device(), y.shape
     for name, t in (("y", y), ("dh", dh), ("out", out)):
-        if t.dtype != torch.bfloat16:
+        if t.dtype is not _BF16:
             raise TypeError(f"{name} must be a CUDA bfloat16 tensor")
-        _same_device(t, y.device, name)
-        if not t.is_contiguous() or t.shape != y.shape:
+        if t.get_device() != dev:
+            _same_device(t, dev, name)
+        if not t.is_contiguous() or t.shape != shape:
             raise ValueError(f"{name} must be contiguous and of y's shape")
     check("ft_gelu_bwd_bf16", load().ft_gelu_bwd_bf16(
-        y.data_ptr(), dh.data_ptr(), out.data_ptr(), y.numel(), _f32(amax_dy, "amax_dy", 1, y.device),
-        _raw_stream(y)))
+        y.data_ptr(), dh.data_ptr(), out.data_ptr(), y.numel(), _f32(amax_dy, "amax_dy", 1, dev), _raw_stream(dev)))
     return out
 
 
@@ -321,50 +346,55 @@ def rope_freqs(axes, theta: float = 10000.0, shared: bool = False, device="cuda"
     return torch.cat([theta ** (-2.0 * torch.arange(a // 2, dtype=torch.float64, device=device) / a) for a in axes])
 
 
-def _rope_view(rope: Rope, pos: torch.Tensor, M: int, S: int, dev) -> FtRope:
-    axes = tuple(rope.axes)
-    if not 1 <= len(axes) <= 4:
+def _rope_view(rope: Rope, pos: torch.Tensor, M: int, S: int, dev: int) -> bytes:
+    axes = rope.axes
+    na, rot = len(axes), sum(axes)
+    if not 1 <= na <= 4:
         raise ValueError("rotary positions have one to four axes")
-    if pos.dtype not in (torch.int32, torch.float32):
+    if pos.dtype is not torch.int32 and pos.dtype is not _F32:
         raise TypeError(f"pos must be int32 or float32, not {pos.dtype}")
-    if tuple(pos.shape) not in ((M, len(axes)),) + (((M,),) if len(axes) == 1 else ()) or not pos.is_contiguous():
-        raise ValueError(f"pos must be contiguous [{M}, {len(axes)}], not {list(pos.shape)}")
-    f = rope.freqs
-    if f.dtype != torch.float64 or f.numel() != sum(axes) // 2 or not f.is_contiguous():
-        raise TypeError(f"freqs must be a contiguous float64 tensor of {sum(axes) // 2}")
+    if (pos.shape != (M, na) and not (na == 1 and pos.shape == (M,))) or not pos.is_contiguous():
+        raise ValueError(f"pos must be contiguous [{M}, {na}], not {list(pos.shape)}")
+    f, wq, wk, hd = rope.freqs, rope.w_q, rope.w_k, rope.head_dim
+    if f.dtype is not torch.float64 or f.numel() != rot // 2 or not f.is_contiguous():
+        raise TypeError(f"freqs must be a contiguous float64 tensor of {rot // 2}")
     pt = None
-    for name, w in (("w_q", rope.w_q), ("w_k", rope.w_k)):
-        if w is None:
-            continue
-        if w.dtype not in _DTYPE or (pt is not None and w.dtype != pt):
-            raise TypeError("w_q and w_k must both be bfloat16 or both float32")
-        if tuple(w.shape) != (rope.head_dim,) or not w.is_contiguous():
-            raise ValueError(f"{name} must be contiguous [{rope.head_dim}]")
-        _same_device(w, dev, name)
-        pt = w.dtype
+    for name, w in (("w_q", wq), ("w_k", wk)):
+        if w is not None:
+            if w.dtype not in _DTYPE or (pt is not None and w.dtype is not pt):
+                raise TypeError("w_q and w_k must both be bfloat16 or both float32")
+            if w.shape != (hd,) or not w.is_contiguous():
+                raise ValueError(f"{name} must be contiguous [{hd}]")
+            _same_device(w, dev, name)
+            pt = w.dtype
     _same_device(pos, dev, "pos")
     _same_device(f, dev, "freqs")
-    return FtRope(M, S, rope.heads, rope.kv_heads, rope.head_dim, len(axes),
-                  (ctypes.c_int32 * 4)(*axes), rope.layout, NORM_RMS if rope.norm else NORM_NONE, rope.eps,
-                  0 if pos.dtype == torch.int32 else 1, _DTYPE[pt or torch.float32], pos.data_ptr(), f.data_ptr(),
-                  _ptr(rope.w_q), _ptr(rope.w_k))
+    return _ROPE.pack(M, S, rope.heads, rope.kv_heads, hd, na, *axes, *(0,) * (4 - na), rope.layout,
+                      NORM_RMS if rope.norm else NORM_NONE, rope.eps, 0 if pos.dtype is torch.int32 else 1,
+                      0 if pt is _BF16 else 1, pos.data_ptr(), f.data_ptr(), _ptr(wq), _ptr(wk))
 
 
-def _heads(t, name: str, B: int, H: int, S: int, hd: int, dev, out: bool) -> FtHeads:
+_NO_HEADS = _HEADS.pack(0, 0, 0, 0)
+
+
+def _heads(t, name: str, shape: tuple, dev: int, out: bool) -> bytes:
     if t is None:
-        return FtHeads(None, 0, 0, 0)
-    if t.dtype != torch.bfloat16:
+        return _NO_HEADS
+    if t.dtype is not _BF16:
         raise TypeError(f"{name} must be a CUDA bfloat16 tensor")
-    _same_device(t, dev, name)
-    if tuple(t.shape) != (B, H, S, hd):
-        raise ValueError(f"{name} must be [{B}, {H}, {S}, {hd}], not {list(t.shape)}")
-    if t.stride(3) != 1:
+    if t.get_device() != dev:
+        _same_device(t, dev, name)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+    sb, sh, st, unit = t.stride()
+    if unit != 1:
         raise ValueError(f"{name} must have unit stride along a head")
+    B, H, S, _ = shape
     # the stride of an axis of one element says nothing
-    st = [t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)]
-    if out and any(t.shape[i] > 1 and st[i] == 0 for i in range(3)):
+    sb, sh, st = sb if B > 1 else 0, sh if H > 1 else 0, st if S > 1 else 0
+    if out and ((B > 1 and sb == 0) or (H > 1 and sh == 0) or (S > 1 and st == 0)):
         raise ValueError(f"{name} is written: its elements must be apart")
-    return FtHeads(t.data_ptr(), *st)
+    return _HEADS.pack(t.data_ptr(), sb, sh, st)
 
 
 @_on_device(1)
@@ -379,31 +409,28 @@ def ft_qk_rope_fwd(rope: Rope, qkv: torch.Tensor, pos: torch.Tensor, *, tokens: 
     among them (in place).  copy_v=False: v is returned as a view of qkv."""
     if qkv.dim() != 2:
         raise ValueError("qkv must be [rows, width]")
-    M, dev = qkv.shape[0], qkv.device
+    M, dev = len(qkv), qkv.get_device()
     S = M if tokens is None else tokens
     if S < 0 or (M > 0 and (S < 1 or M % S)):
         raise ValueError(f"{M} rows are no samples of {S} tokens")
     B = M // S if S else 0
-    ld = _matrix(qkv, "qkv", torch.bfloat16, M, rope.width, dev)
+    Hq, Hk, hd = rope.heads, rope.kv_heads, rope.head_dim
+    ld = _matrix(qkv, "qkv", _BF16, M, rope.width, dev)
 
     def new(H):
-        if head_major:
-            return torch.empty(B, H, S, rope.head_dim, dtype=torch.bfloat16, device=dev)
-        return torch.empty(B, S, H, rope.head_dim, dtype=torch.bfloat16, device=dev).transpose(1, 2)
+        return qkv.new_empty((B, H, S, hd)) if head_major else qkv.new_empty((B, S, H, hd)).transpose(1, 2)
 
     view = _rope_view(rope, pos, M, S, dev)
-    q = new(rope.heads) if q is None else q
-    k = new(rope.kv_heads) if k is None else k
+    q = new(Hq) if q is None else q
+    k = new(Hk) if k is None else k
     if v is None and copy_v:
-        v = new(rope.kv_heads)
-    hq = _heads(q, "q", B, rope.heads, S, rope.head_dim, dev, True)
-    hk = _heads(k, "k", B, rope.kv_heads, S, rope.head_dim, dev, True)
-    hv = _heads(v, "v", B, rope.kv_heads, S, rope.head_dim, dev, True)
-    check("ft_qk_rope_fwd", load().ft_qk_rope_fwd(ctypes.byref(view), qkv.data_ptr(), ld, ctypes.byref(hq),
-                                                  ctypes.byref(hk), ctypes.byref(hv), _raw_stream(qkv)))
+        v = new(Hk)
+    hq = _heads(q, "q", (B, Hq, S, hd), dev, True)
+    hk = _heads(k, "k", (B, Hk, S, hd), dev, True)
+    hv = _heads(v, "v", (B, Hk, S, hd), dev, True)
+    check("ft_qk_rope_fwd", load().ft_qk_rope_fwd(view, qkv.data_ptr(), ld, hq, hk, hv, _raw_stream(dev)))
     if v is None:
-        v = qkv[:, (rope.heads + rope.kv_heads) * rope.head_dim:].unflatten(1, (rope.kv_heads, rope.head_dim))
-        v = v.unflatten(0, (B, S)).transpose(1, 2)
+        v = qkv[:, (Hq + Hk) * hd:].unflatten(1, (Hk, hd)).unflatten(0, (B, S)).transpose(1, 2)
     return q, k, v
 
 
@@ -419,25 +446,27 @@ def ft_qk_rope_bwd(rope: Rope, dq: torch.Tensor, dk: torch.Tensor, dv: torch.Ten
     if dq.dim() != 4:
         raise ValueError("dq must be [samples, heads, tokens, head_dim]")
     B, _, S, _ = dq.shape
-    M, dev = B * S, dq.device
+    M, dev = B * S, dq.get_device()
+    Hq, Hk, hd = rope.heads, rope.kv_heads, rope.head_dim
     if rope.norm and qkv is None:
         raise ValueError("the gradient through the norm needs qkv")
     view = _rope_view(rope, pos, M, S, dev)
-    ld = 0 if qkv is None else _matrix(qkv, "qkv", torch.bfloat16, M, rope.width, dev)
+    ld = 0 if qkv is None else _matrix(qkv, "qkv", _BF16, M, rope.width, dev)
     if dqkv is None:
-        new = torch.zeros if dv is None else torch.empty
-        dqkv = new(M, rope.width, dtype=torch.bfloat16, device=dev)
-    ldd = _matrix(dqkv, "dqkv", torch.bfloat16, M, rope.width, dev)
-    hq = _heads(dq, "dq", B, rope.heads, S, rope.head_dim, dev, False)
-    hk = _heads(dk, "dk", B, rope.kv_heads, S, rope.head_dim, dev, False)
-    hv = _heads(dv, "dv", B, rope.kv_heads, S, rope.head_dim, dev, False)
-    dw = [torch.empty(rope.head_dim, dtype=torch.float32, device=dev)
-          if weight_grads and rope.norm and w is not None else None for w in (rope.w_q, rope.w_k)]
-    buf = None
-    if dw[0] is not None or dw[1] is not None:
-        buf = _scratch(ws, load().ft_qk_rope_workspace_bytes(M, rope.head_dim), dev)
+        dqkv = (dq.new_zeros if dv is None else dq.new_empty)((M, rope.width))
+    ldd = _matrix(dqkv, "dqkv", _BF16, M, rope.width, dev)
+    hq = _heads(dq, "dq", (B, Hq, S, hd), dev, False)
+    hk = _heads(dk, "dk", (B, Hk, S, hd), dev, False)
+    hv = _heads(dv, "dv", (B, Hk, S, hd), dev, False)
+    dw_q = dw_k = buf = None
+    nws = 0
+    if weight_grads and rope.norm:
+        dw_q = None if rope.w_q is None else dq.new_empty(hd, dtype=_F32)
+        dw_k = None if rope.w_k is None else dq.new_empty(hd, dtype=_F32)
+        if dw_q is not None or dw_k is not None:
+            nws = load().ft_qk_rope_workspace_bytes(M, hd)
+            buf = _scratch(ws, nws, dq)
     check("ft_qk_rope_bwd", load().ft_qk_rope_bwd(
-        ctypes.byref(view), ctypes.byref(hq), ctypes.byref(hk), ctypes.byref(hv), _ptr(qkv), ld, dqkv.data_ptr(), ldd,
-        _ptr(dw[0]), _ptr(dw[1]), _f32(amax, "amax", 1, dev), _ptr(buf), 0 if buf is None else buf.numel(),
-        _raw_stream(dq)))
-    return dqkv, dw[0], dw[1]
+        view, hq, hk, hv, _ptr(qkv), ld, dqkv.data_ptr(), ldd, _ptr(dw_q), _ptr(dw_k), _f32(amax, "amax", 1, dev),
+        _ptr(buf), nws, _raw_stream(dev)))
+    return dqkv, dw_q, dw_k

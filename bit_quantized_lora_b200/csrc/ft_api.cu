@@ -12,7 +12,9 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <map>
 #include <mutex>
+#include <tuple>
 #include <vector>
 
 #include "../../include/ft.h"
@@ -40,6 +42,9 @@ struct DevInfo {
     bool attr_set = false;
     int qres_ctas = 0;  // CTAs of k_qres that fit on the device at once
     unsigned long long ctx = 0;  // the context the kernel attributes were set in
+    // of launches with dynamic shared memory, by kernel, threads and bytes:
+    // blocks that an SM holds (asking takes longer than the launch)
+    std::map<std::tuple<const void*, int, size_t>, int> per_sm;
 };
 DevInfo g_dev[64];
 std::mutex g_mu;
@@ -82,7 +87,10 @@ ft_status device_info(DevInfo** out) {
     DevInfo& d = g_dev[dev];
     unsigned long long ctx = 0;
     if (current_ctx_id(dev, &ctx) != FT_OK) return FT_ERR_CUDA;
-    if (d.attr_set && d.ctx != ctx) d.attr_set = false;  // a new context: set the attributes again
+    if (d.attr_set && d.ctx != ctx) {  // a new context: set the attributes again
+        d.attr_set = false;
+        d.per_sm.clear();
+    }
     if (!d.init) {
         int major = 0, minor = 0, sms = 0;
         if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||

@@ -83,19 +83,36 @@ ft_status check_norm(const ft_gated_norm* n) {
     return FT_OK;
 }
 
+uint32_t norm_has(const ft_gated_norm* n) {
+    using namespace ft::norm;
+    return (n->gate ? kGate : 0u) | (n->scale ? kScale : 0u) | (n->shift ? kShift : 0u) | (n->w ? kW : 0u) |
+           (n->bias ? kBias : 0u) | (n->w_post ? kWPost : 0u) | (n->pre != FT_NORM_NONE ? kPre : 0u) |
+           (n->pre == FT_NORM_LAYER ? kPreMean : 0u) | (n->post != FT_NORM_NONE ? kPost : 0u) |
+           (n->post == FT_NORM_LAYER ? kPostMean : 0u);
+}
+// Blocks of `k` that an SM holds; lets the kernel take its shared memory
+// first.  Asked once per kernel and launch shape in a context.
+ft_status blocks_per_sm(const void* k, int threads, size_t smem, DevInfo* d, int* out) {
+    std::lock_guard<std::mutex> lk(g_mu);
+    int& n = d->per_sm[std::make_tuple(k, threads, smem)];
+    if (n == 0) {
+        int got = 0;
+        if (smem > 32 * 1024)  // with the static part, above what a launch may take unasked
+            FT_TRY(cuda_ok(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)));
+        FT_TRY(cuda_ok(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&got, k, threads, smem)));
+        n = std::max(1, got);
+    }
+    *out = n;
+    return FT_OK;
+}
 // Launches `k` with `smem` bytes of dynamic shared memory per block, the grid
 // cut to the blocks that the device holds at once when `resident` is set.
 template <typename P>
 ft_status launch_norm(void (*k)(P), const P& p, int grid, bool resident, int threads, size_t smem, DevInfo* d,
                       cudaStream_t st) {
-    if (smem > 32 * 1024)  // with the static part, above what a launch may take unasked
-        FT_TRY(cuda_ok(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)));
-    if (resident && grid > d->sms) {
-        int per_sm = 0;
-        FT_TRY(cuda_ok(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, threads, smem)));
-        // blocks with the same number of turns
-        grid = cdiv(grid, cdiv(grid, std::max(1, per_sm) * d->sms));
-    }
+    int per_sm = 1;
+    FT_TRY(blocks_per_sm(reinterpret_cast<const void*>(k), threads, smem, d, &per_sm));
+    if (resident && grid > d->sms) grid = cdiv(grid, cdiv(grid, per_sm * d->sms));  // the same number of turns each
     return launch_overlapped(k, grid, threads, smem, st, p);
 }
 template <typename XT, int V, bool kWide, bool k32>
@@ -116,17 +133,20 @@ ft_status launch_norm_bwd(const ft::norm::BwdParams& p, const RowShape& s, int g
         if (mod) return launch_norm(k_gated_norm_bwd<XT, V, kWide, k32, true>, p, grid, false, s.threads, smem, d, st);
     return launch_norm(k_gated_norm_bwd<XT, V, kWide, k32, false>, p, grid, false, s.threads, smem, d, st);
 }
+constexpr uint32_t kFwdMod = ft::norm::kY | ft::norm::kGate | ft::norm::kScale | ft::norm::kShift | ft::norm::kPre;
+constexpr uint32_t kBwdMod = ft::norm::kDh | ft::norm::kDr | ft::norm::kR | ft::norm::kY | ft::norm::kGate |
+                             ft::norm::kScale | ft::norm::kDx | ft::norm::kDy | ft::norm::kPre | ft::norm::kStats;
+constexpr uint32_t kNotMod = ft::norm::kW | ft::norm::kBias | ft::norm::kWPost | ft::norm::kPost;
 template <typename XT, bool k32>
 ft_status launch_norm(const ft::norm::FwdParams& p, const RowShape& s, int grid, DevInfo* d, cudaStream_t st) {
-    const bool mod = p.y && p.gate && p.scale && p.shift && !p.w && !p.bias && !p.w_post && p.post == FT_NORM_NONE;
+    const bool mod = (p.has & kFwdMod) == kFwdMod && !(p.has & kNotMod);
     if (!s.wide) return launch_norm_fwd<XT, 1, false, k32>(p, s, grid, false, d, st);
     if (s.v == 1) return launch_norm_fwd<XT, 1, true, k32>(p, s, grid, mod, d, st);
     if (s.v == 2) return launch_norm_fwd<XT, 2, true, k32>(p, s, grid, mod, d, st);
     return launch_norm_fwd<XT, 4, true, k32>(p, s, grid, mod, d, st);
 }
 bool norm_bwd_mod(const ft::norm::BwdParams& p) {
-    return p.dh && p.dr && p.r && p.y && p.gate && p.scale && p.dx && p.dy && !p.w && !p.w_post &&
-           p.post == FT_NORM_NONE;
+    return (p.has & kBwdMod) == kBwdMod && !(p.has & kNotMod);
 }
 template <typename XT, bool k32>
 ft_status launch_norm(const ft::norm::BwdParams& p, const RowShape& s, int grid, DevInfo* d, cudaStream_t st) {
@@ -231,12 +251,13 @@ int rope_grid(ft::rope::Params* p) {
     return (int)std::min<int64_t>(((int64_t)p->M * p->slices + kWarps - 1) / kWarps, blocks);
 }
 template <bool kBwd>
-ft_status launch_rope(const ft::rope::Params& p, int grid, cudaStream_t st) {
+ft_status launch_rope(const ft::rope::Params& p, int grid, DevInfo* d, cudaStream_t st) {
     using namespace ft::rope;
     auto* k = p.halves ? (p.norm ? k_qk_rope<kBwd, true, true> : k_qk_rope<kBwd, true, false>)
                        : (p.norm ? k_qk_rope<kBwd, false, true> : k_qk_rope<kBwd, false, false>);
     const size_t smem = p.norm ? kRingBytes<kBwd, true> : kRingBytes<kBwd, false>;
-    if (smem) FT_TRY(cuda_ok(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)));
+    int per_sm = 1;
+    if (smem) FT_TRY(blocks_per_sm(reinterpret_cast<const void*>(k), kThreads, smem, d, &per_sm));
     return launch_overlapped(k, grid, kThreads, smem, st, p);
 }
 
@@ -328,8 +349,6 @@ ft_status ft_gated_norm_fwd(const ft_gated_norm* n, const void* x, int64_t ldx, 
     p.B = (int)n->B;
     p.S = (int)(n->M / n->B);
     p.offsets = n->offsets;
-    p.pre = n->pre;
-    p.post = n->post;
     p.eps_pre = n->eps_pre;
     p.eps_post = n->eps_post;
     p.alpha = n->alpha;
@@ -355,6 +374,7 @@ ft_status ft_gated_norm_fwd(const ft_gated_norm* n, const void* x, int64_t ldx, 
     p.stats = reinterpret_cast<float4*>(stats);
     p.amax = amax_h;
     p.tpr = s.tpr;
+    p.has = norm_has(n) | (y ? ft::norm::kY : 0u) | (stats ? ft::norm::kStats : 0u);
     const int per = s.wide ? 1 : s.threads / s.tpr;
     const int grid = cdiv(n->M, per);
     LaunchTimer lt(KID_NORM_FWD, st);
@@ -408,8 +428,6 @@ ft_status ft_gated_norm_bwd(const ft_gated_norm* n, const void* dh, int64_t lddh
         p.B = (int)n->B;
         p.S = (int)(n->M / n->B);
         p.offsets = n->offsets;
-        p.pre = n->pre;
-        p.post = n->post;
         p.alpha = n->alpha;
         p.inv_d = 1.0f / (float)n->D;
         p.p32 = n->pt == FT_F32;
@@ -436,6 +454,9 @@ ft_status ft_gated_norm_bwd(const ft_gated_norm* n, const void* dh, int64_t lddh
         p.partial = static_cast<float*>(ws);
         p.need_s = need_s;
         p.need_t = need_t;
+        p.has = norm_has(n) | (dh ? ft::norm::kDh : 0u) | (dr ? ft::norm::kDr : 0u) | (p.r ? ft::norm::kR : 0u) |
+                (p.y ? ft::norm::kY : 0u) | (g->dx ? ft::norm::kDx : 0u) | (g->dy ? ft::norm::kDy : 0u) |
+                (p.stats ? ft::norm::kStats : 0u);
         chunk = norm_bwd_chunk(n->M, n->D, norm_bwd_mod(p));
         p.chunk = (int)chunk;
         p.tpr = s.tpr;
@@ -473,13 +494,15 @@ ft_status ft_gated_norm_bwd(const ft_gated_norm* n, const void* dh, int64_t lddh
     q.need_t = need_t;
     if (g->dw_post || g->dw || g->dbias) q.sums = static_cast<float*>(ws) + norm_bwd_partials(n->M, n->D, n->B);
     LaunchTimer lt(KID_NORM_REDUCE, st);
-    ft_status e = launch_overlapped(ft::norm::k_gated_norm_reduce,
-                                    dim3(cdiv(n->D, 32), (unsigned)std::min<int64_t>(n->B, 32768)),
-                                    32 * ft::norm::kReduceGroups, 0, st, q);
+    // partial rows of a sample of average length
+    const bool few = n->M / chunk / n->B < 8;
+    const dim3 grid(cdiv(n->D, 32), (unsigned)std::min<int64_t>(n->B, 32768));
+    ft_status e = few ? launch_overlapped(ft::norm::k_gated_norm_reduce<4>, grid, 128, 0, st, q)
+                      : launch_overlapped(ft::norm::k_gated_norm_reduce<32>, grid, 1024, 0, st, q);
     lt.stop();
     if (e != FT_OK || !q.sums) return e;
     LaunchTimer lt2(KID_NORM_WEIGHTS, st);
-    e = launch_overlapped(ft::norm::k_gated_norm_weights, cdiv(n->D, 64), 64, 0, st, q);
+    e = launch_overlapped(ft::norm::k_gated_norm_weights, cdiv(n->D, 32), 32, 0, st, q);
     lt2.stop();
     return e;
 }
@@ -523,7 +546,7 @@ ft_status ft_qk_rope_fwd(const ft_rope* R, const void* qkv, int64_t ld, const ft
     p.ld = ld;
     LaunchTimer lt(KID_ROPE_FWD, st);
     const int grid = rope_grid<false>(&p);
-    const ft_status e = launch_rope<false>(p, grid, st);
+    const ft_status e = launch_rope<false>(p, grid, d, st);
     lt.stop();
     return e;
 }
@@ -564,7 +587,7 @@ ft_status ft_qk_rope_bwd(const ft_rope* R, const ft_heads* dq, const ft_heads* d
         p.partial = dw ? static_cast<float*>(ws) : nullptr;
         blocks = rope_grid<true>(&p);
         LaunchTimer lt(KID_ROPE_BWD, st);
-        const ft_status e = launch_rope<true>(p, blocks, st);
+        const ft_status e = launch_rope<true>(p, blocks, d, st);
         lt.stop();
         FT_TRY(e);
     }

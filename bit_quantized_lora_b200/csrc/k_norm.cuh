@@ -29,10 +29,17 @@
 namespace ft {
 namespace norm {
 
+// What a call has, as bits: one test of a word each, where comparing pointers
+// and kinds took the general kernels a third of their instructions.
+enum Has : uint32_t {
+    kDh = 1, kDr = 2, kR = 4, kY = 8, kGate = 16, kScale = 32, kShift = 64, kW = 128, kBias = 256, kWPost = 512,
+    kPre = 1024, kPreMean = 2048, kPost = 4096, kPostMean = 8192, kDx = 16384, kDy = 32768, kStats = 65536
+};
+
 struct FwdParams {
+    uint32_t has;
     int M, D, B, S;  // S: rows per sample when there are no offsets
     const int32_t* offsets;
-    int pre, post;
     float eps_pre, eps_post, alpha, inv_d;
     bool p32;
     int64_t ld_gate, ld_scale, ld_shift;
@@ -51,9 +58,9 @@ struct FwdParams {
 };
 
 struct BwdParams {
+    uint32_t has;
     int M, D, B, S;
     const int32_t* offsets;
-    int pre, post;
     float alpha, inv_d;
     bool p32;
     int64_t ld_gate, ld_scale;
@@ -180,11 +187,10 @@ __device__ __forceinline__ void ring_copy(uint32_t dst, int slot_stride, const T
 // Mean and 1/deviation of a row held as V vectors of eight (`ok[v]`: this
 // thread has a vector v); leaves x - mean in x.
 template <int V, bool kWide>
-__device__ __forceinline__ float2 center(F8 (&x)[V], const bool (&ok)[V], int kind, float eps, float inv_d,
+__device__ __forceinline__ float2 center(F8 (&x)[V], const bool (&ok)[V], bool about_mean, float eps, float inv_d,
                                          RowSum<kWide>& sum) {
     float mean = 0.0f;
-    if (kind == FT_NORM_NONE) return make_float2(0.0f, 1.0f);
-    if (kind == FT_NORM_LAYER) {
+    if (about_mean) {
         float2 s = both(0.0f);
 #pragma unroll
         for (int v = 0; v < V; ++v) s = gather(s, x[v]);  // absent vectors are zeros
@@ -210,7 +216,7 @@ constexpr int kFwdSlots = sizeof(XT) / 2 + 1;  // x, y
 // spends on asking for each part is then a third of its instructions less.
 template <typename XT, int V, bool kWide, bool k32, bool kMod>
 __global__ void __launch_bounds__(256) k_gated_norm_fwd(const __grid_constant__ FwdParams p) {
-    constexpr int kY = sizeof(XT) / 2;
+    constexpr int kYSlot = sizeof(XT) / 2;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) float red[kRedFloats];
     const int tpr = kWide ? blockDim.x : p.tpr;
@@ -227,9 +233,10 @@ __global__ void __launch_bounds__(256) k_gated_norm_fwd(const __grid_constant__ 
         at[v] = ok[v] ? col[v] : 0;
     }
     ring.clear(kFwdStages);
-    const bool has_y = kMod || p.y, has_gate = kMod || p.gate, has_scale = kMod || p.scale, has_shift = kMod || p.shift;
-    const bool has_w = !kMod && p.w, has_bias = !kMod && p.bias, has_wp = !kMod && p.w_post;
-    const bool has_post = !kMod && p.post != FT_NORM_NONE, has_pre = kMod || p.pre != FT_NORM_NONE;
+    const uint32_t has = p.has;
+    const bool has_y = kMod || has & kY, has_gate = kMod || has & kGate, has_scale = kMod || has & kScale;
+    const bool has_shift = kMod || has & kShift, has_w = !kMod && has & kW, has_bias = !kMod && has & kBias;
+    const bool has_wp = !kMod && has & kWPost, has_post = !kMod && has & kPost, has_pre = kMod || has & kPre;
     grid_dep_launch();
     grid_dep_wait();
     const int step = gridDim.x * groups;
@@ -241,7 +248,7 @@ __global__ void __launch_bounds__(256) k_gated_norm_fwd(const __grid_constant__ 
             for (int v = 0; v < V; ++v)
                 if (ok[v]) {
                     ring_copy(ring.at(stage, v, 0), ring.slot_stride, x + col[v]);
-                    if (has_y) ring_copy(ring.at(stage, v, kY), ring.slot_stride, y + col[v]);
+                    if (has_y) ring_copy(ring.at(stage, v, kYSlot), ring.slot_stride, y + col[v]);
                 }
         }
         cp_async_commit();
@@ -263,8 +270,8 @@ __global__ void __launch_bounds__(256) k_gated_norm_fwd(const __grid_constant__ 
         F8 f[V];
         if (has_y) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) f[v] = ring.get(stage, v, kY, live, __nv_bfloat16());
-            if (has_post) post = center<V, kWide>(f, ok, p.post, p.eps_post, p.inv_d, sum);
+            for (int v = 0; v < V; ++v) f[v] = ring.get(stage, v, kYSlot, live, __nv_bfloat16());
+            if (has_post) post = center<V, kWide>(f, ok, has & kPostMean, p.eps_post, p.inv_d, sum);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 if (has_post) f[v] = mul(f[v], post.y);
@@ -281,7 +288,8 @@ __global__ void __launch_bounds__(256) k_gated_norm_fwd(const __grid_constant__ 
 #pragma unroll
             for (int v = 0; v < V; ++v) f[v] = ring.get(stage, v, 0, live, XT());
         }
-        const float2 pre = center<V, kWide>(f, ok, p.pre, p.eps_pre, p.inv_d, sum);
+        const float2 pre = has_pre ? center<V, kWide>(f, ok, has & kPreMean, p.eps_pre, p.inv_d, sum)
+                                   : make_float2(0.0f, 1.0f);
         if (!live) continue;
         if (has_pre) {
 #pragma unroll
@@ -301,7 +309,7 @@ __global__ void __launch_bounds__(256) k_gated_norm_fwd(const __grid_constant__ 
                 if (ok[v]) amax = store8_max(p.h + (int64_t)row * p.ldh + col[v], f[v], amax);
             }
         }
-        if (p.stats && t == 0) p.stats[row] = make_float4(pre.x, pre.y, post.x, post.y);
+        if (has & kStats && t == 0) p.stats[row] = make_float4(pre.x, pre.y, post.x, post.y);
     }
     cp_async_wait<0>();
     raise_amax(p.amax, amax_of(amax), red);
@@ -316,13 +324,13 @@ template <typename XT>
 constexpr int kBwdSlots = 2 + 2 * (sizeof(XT) / 2);  // dh, y, dr, r
 constexpr int kBwdStages = 2;
 template <int V, bool kWide, bool kMod>
-constexpr int kBwdRegs = V == 2 ? 96 : kWide ? (kMod ? 80 : 56) : 128;
+constexpr int kBwdRegs = V == 2 ? 96 : kWide ? (kMod ? 80 : 64) : 128;
 
 // kMod: dh, dr, r, y, gate and scale given, dx and dy wanted, no weights, no
 // post norm; as in the forward.
 template <typename XT, int V, bool kWide, bool k32, bool kMod>
 __global__ void __maxnreg__((kBwdRegs<V, kWide, kMod>)) k_gated_norm_bwd(const __grid_constant__ BwdParams p) {
-    constexpr int kStages = kBwdStages, kDr = 2, kR = 2 + sizeof(XT) / 2;
+    constexpr int kStages = kBwdStages, kDrSlot = 2, kRSlot = 2 + sizeof(XT) / 2;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) float red[kRedFloats];
     __shared__ __align__(16) float flush_buf[kWide ? 1 : 256 * 8];
@@ -340,10 +348,11 @@ __global__ void __maxnreg__((kBwdRegs<V, kWide, kMod>)) k_gated_norm_bwd(const _
         pat[v] = ok[v] ? col[v] : 0;
     }
     ring.clear(kStages);
-    const bool has_dh = kMod || p.dh, has_dr = kMod || p.dr, has_r = kMod || p.r, has_y = kMod || p.y;
-    const bool has_gate = kMod || p.gate, has_scale = kMod || p.scale, has_w = !kMod && p.w, has_wp = !kMod && p.w_post;
-    const bool pre = kMod || p.pre != FT_NORM_NONE, post = !kMod && p.post != FT_NORM_NONE;
-    const bool want_dx = kMod || p.dx, want_dy = kMod || p.dy, through = want_dy && post;
+    const uint32_t has = p.has;
+    const bool has_dh = kMod || has & kDh, has_dr = kMod || has & kDr, has_r = kMod || has & kR, has_y = kMod || has & kY;
+    const bool has_gate = kMod || has & kGate, has_scale = kMod || has & kScale, has_w = !kMod && has & kW;
+    const bool has_wp = !kMod && has & kWPost, pre = kMod || has & kPre, post = !kMod && has & kPost;
+    const bool want_dx = kMod || has & kDx, want_dy = kMod || has & kDy, through = want_dy && post;
     const int begin = blockIdx.x * p.chunk, end = min(p.M, begin + p.chunk);
     const int turns = (end - begin + groups - 1) / groups;
     grid_dep_launch();
@@ -357,10 +366,10 @@ __global__ void __maxnreg__((kBwdRegs<V, kWide, kMod>)) k_gated_norm_bwd(const _
                 if (has_dh) ring_copy(ring.at(stage, v, 0), 0, p.dh + (int64_t)row * p.lddh + col[v]);
                 if (has_y) ring_copy(ring.at(stage, v, 1), 0, p.y + (int64_t)row * p.ldy + col[v]);
                 if (has_dr)
-                    ring_copy(ring.at(stage, v, kDr), ring.slot_stride,
+                    ring_copy(ring.at(stage, v, kDrSlot), ring.slot_stride,
                               static_cast<const XT*>(p.dr) + (int64_t)row * p.lddr + col[v]);
                 if (has_r)
-                    ring_copy(ring.at(stage, v, kR), ring.slot_stride,
+                    ring_copy(ring.at(stage, v, kRSlot), ring.slot_stride,
                               static_cast<const XT*>(p.r) + (int64_t)row * p.ldr + col[v]);
             }
         }
@@ -369,7 +378,7 @@ __global__ void __maxnreg__((kBwdRegs<V, kWide, kMod>)) k_gated_norm_bwd(const _
     float4 nst = make_float4(0.0f, 1.0f, 0.0f, 1.0f);
     auto fetch_stats = [&](int turn) {
         const int row = begin + turn * groups + group;
-        if ((kMod || p.stats) && row < end) nst = __ldg(p.stats + row);
+        if ((kMod || has & kStats) && row < end) nst = __ldg(p.stats + row);
     };
     F8 acc[3][V];
 #pragma unroll
@@ -440,7 +449,7 @@ __global__ void __maxnreg__((kBwdRegs<V, kWide, kMod>)) k_gated_norm_bwd(const _
                 float2 s0 = both(0.0f), s1 = both(0.0f);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    const F8 xh = mul(add(ring.get(stage, v, kR, live, XT()), live ? -st.x : 0.0f), live ? st.y : 0.0f);
+                    const F8 xh = mul(add(ring.get(stage, v, kRSlot, live, XT()), live ? -st.x : 0.0f), live ? st.y : 0.0f);
                     z[v] = ring.get(stage, v, 0, live, __nv_bfloat16());
                     acc[0][v] = add(acc[0][v], z[v]);
                     acc[1][v] = fma(z[v], xh, acc[1][v]);
@@ -450,7 +459,7 @@ __global__ void __maxnreg__((kBwdRegs<V, kWide, kMod>)) k_gated_norm_bwd(const _
                     s1 = gather(s1, z[v], xh);
                 }
                 const float2 m = sum(make_float2(s0.x + s0.y, s1.x + s1.y));
-                a0 = p.pre == FT_NORM_LAYER && live ? -m.x * p.inv_d * st.y : 0.0f;
+                a0 = has & kPreMean && live ? -m.x * p.inv_d * st.y : 0.0f;
                 a1 = live ? -m.y * p.inv_d * st.y * st.y : 0.0f;
             }
             auto normed_y = [&](int v) {
@@ -461,10 +470,10 @@ __global__ void __maxnreg__((kBwdRegs<V, kWide, kMod>)) k_gated_norm_bwd(const _
             F8 e[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                e[v] = has_dr ? ring.get(stage, v, kDr, live, XT()) : zero8();
+                e[v] = has_dr ? ring.get(stage, v, kDrSlot, live, XT()) : zero8();
                 if (pre) {
                     // the row is read again rather than kept: registers set how many blocks an SM holds
-                    const F8 xc = add(ring.get(stage, v, kR, live, XT()), live ? -st.x : 0.0f);
+                    const F8 xc = add(ring.get(stage, v, kRSlot, live, XT()), live ? -st.x : 0.0f);
                     e[v] = add(fma(xc, a1, fma(z[v], live ? st.y : 0.0f, e[v])), a0);
                 }
                 F8 yh = zero8();
@@ -495,7 +504,7 @@ __global__ void __maxnreg__((kBwdRegs<V, kWide, kMod>)) k_gated_norm_bwd(const _
             }
             if (through) {
                 const float2 m = sum(make_float2(s0.x + s0.y, s1.x + s1.y));
-                const float e0 = p.post == FT_NORM_LAYER ? m.x * p.inv_d : 0.0f, e1 = m.y * p.inv_d;
+                const float e0 = has & kPostMean ? m.x * p.inv_d : 0.0f, e1 = m.y * p.inv_d;
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     if (!ok[v] || !live) continue;
@@ -528,12 +537,12 @@ struct ReduceParams {
 };
 
 // Adds the partial rows of each sample in a fixed order: 32 columns per
-// block, a thread per column and every kReduceGroups-th partial row, so that
-// all of a thread's loads are in flight at once.  Sample b's partial rows
-// are those of the chunks that hold its rows.
-constexpr int kReduceGroups = 32;
-__global__ void __launch_bounds__(32 * kReduceGroups) k_gated_norm_reduce(const __grid_constant__ ReduceParams p) {
-    __shared__ float part[3][kReduceGroups][33];
+// block, a thread per column and every kGroups-th partial row (32, or 4 where
+// samples have few), so that a thread's loads are in flight at once.  Sample
+// b's partial rows are those of the chunks that hold its rows.
+template <int kGroups>
+__global__ void __launch_bounds__(32 * kGroups) k_gated_norm_reduce(const __grid_constant__ ReduceParams p) {
+    __shared__ float part[3][kGroups][33];
     const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
     const bool ok = c < p.D;
@@ -551,9 +560,9 @@ __global__ void __launch_bounds__(32 * kReduceGroups) k_gated_norm_reduce(const 
         if (ok && lo < hi) {
             const int c0 = lo / p.chunk, c1 = (hi - 1) / p.chunk;
             const float* q = p.partial + ((int64_t)c0 + b + g) * 3 * p.D + c;
-            const int64_t step = (int64_t)kReduceGroups * 3 * p.D;
+            const int64_t step = (int64_t)kGroups * 3 * p.D;
 #pragma unroll 4
-            for (int k = c0 + g; k <= c1; k += kReduceGroups, q += step) {
+            for (int k = c0 + g; k <= c1; k += kGroups, q += step) {
                 if (p.need_s) {
                     s[0] += __ldg(q);
                     s[1] += __ldg(q + p.D);
@@ -565,11 +574,10 @@ __global__ void __launch_bounds__(32 * kReduceGroups) k_gated_norm_reduce(const 
 #pragma unroll
         for (int k = 0; k < 3; ++k) part[k][g][lane] = s[k];
         __syncthreads();
-        // warp k adds sum k: a column per lane
-        if (g < 3) {
+        if (g < 3) {  // warp k adds sum k
             float t = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kReduceGroups; ++i) t += part[g][i][lane];
+            for (int i = 0; i < kGroups; ++i) t += part[g][i][lane];
             part[g][0][lane] = t;
         }
         __syncthreads();
@@ -590,8 +598,9 @@ __global__ void __launch_bounds__(32 * kReduceGroups) k_gated_norm_reduce(const 
 }
 
 // The weights' gradients from the samples' sums.
-__global__ void __launch_bounds__(64) k_gated_norm_weights(const __grid_constant__ ReduceParams p) {
-    const int c = blockIdx.x * 64 + threadIdx.x;
+__global__ void __launch_bounds__(32) k_gated_norm_weights(const __grid_constant__ ReduceParams p) {
+    const int c = blockIdx.x * 32 + threadIdx.x;
+    grid_dep_launch();
     grid_dep_wait();
     if (c >= p.D) return;
     float dw = 0.0f, db = 0.0f, dwp = 0.0f;

@@ -8,16 +8,18 @@
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import numpy as np
 import torch
 
-from ._lib import FtAdamwHyper, FtAdamwTensor, check, load
+from ._lib import FtAdamwTensor, check, load
 from .blockops import _DTYPE, _f32, _on_device, _raw_stream
 
 BLOCK = 256  # consecutive values that share a scale of an 8-bit state
 _RECORD = np.dtype([("p", "u8"), ("p16", "u8"), ("grad", "u8"), ("m", "u8"), ("v", "u8"), ("m_scale", "u8"),
                     ("v_scale", "u8"), ("n", "i8"), ("weight_decay", "f4"), ("gt", "i4")])
+_HYPER = struct.Struct("@4d")  # ft_adamw_hyper
 assert _RECORD.itemsize == ctypes.sizeof(FtAdamwTensor)
 
 
@@ -29,9 +31,10 @@ def ft_adamw_decode(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor
         raise TypeError("codes must be a contiguous int8 or uint8 tensor")
     n = codes.numel()
     out = torch.empty(codes.shape, dtype=torch.float32, device=codes.device) if out is None else out
+    dev = codes.get_device()
     check("ft_adamw_decode", load().ft_adamw_decode(
-        codes.data_ptr(), _f32(scales, "scales", -(-n // BLOCK), codes.device), n, int(codes.dtype == torch.uint8),
-        _f32(out, "out", n, codes.device), _raw_stream(codes)))
+        codes.data_ptr(), _f32(scales, "scales", -(-n // BLOCK), dev), n, int(codes.dtype == torch.uint8),
+        _f32(out, "out", n, dev), _raw_stream(dev)))
     return out
 
 
@@ -93,6 +96,10 @@ class AdamW:
         self._rec = np.zeros(len(self.params), _RECORD)
         self._rec["n"] = [p.numel() for p in self.params]
         self._rec["weight_decay"] = decay
+        self._rec_addr = self._rec.ctypes.data
+        self._all16, self._all_master = bool(self._is16.all()), bool(self._has_master.all())
+        self._bind()
+        self._lent = False
         self.grads = None if grads is None else self._checked(grads)
 
     def _checked(self, grads) -> list:
@@ -104,6 +111,7 @@ class AdamW:
                 raise TypeError("gradients must be bfloat16 or float32")
             if g.shape != p.shape or not g.is_contiguous() or g.device != p.device:
                 raise ValueError("a gradient must be contiguous, of its parameter's shape and on its device")
+        self._rec["gt"] = [_DTYPE[g.dtype] for g in grads]
         return grads
 
     def step(self, grads=None, lr=None, grad_scale: torch.Tensor | None = None, stream=None) -> None:
@@ -111,27 +119,25 @@ class AdamW:
         float32 device scalar (a captured step whose rate changes), in place
         of the optimizer's.  grad_scale: a float32 device scalar that
         multiplies the gradients (1 / ranks, a clipping factor)."""
-        grads = self.grads if grads is None else self._checked(grads)
-        if grads is None:
+        if grads is not None:
+            grads = self._checked(grads)
+        elif self.grads is not None:
+            grads = self.grads
+            if self._lent:  # the last step read others
+                self._checked(grads)
+        else:
             raise ValueError("step() needs gradients")
+        self._lent = grads is not self.grads
         self._launch(self._step, grads, self.lr if lr is None else lr, grad_scale, stream=stream)
 
     @staticmethod
     def _ptrs(ts) -> np.ndarray:
         return np.array([t.data_ptr() for t in ts], np.uint64)
 
-    def _launch(self, *args, stream=None) -> None:
-        return _on_device(0)(self._launch_here)(*args, stream=stream)
-
-    def _launch_here(self, step, grads, lr, grad_scale) -> None:
-        rec, dev = self._rec, step.device
-        at = self._starts
-        own = self._ptrs(self.params)
-        rec["p16"] = np.where(self._is16, own, 0)
-        master = at * np.uint64(4) + np.uint64(0 if self.master is None else self.master.data_ptr())
-        rec["p"] = np.where(self._has_master, master, np.where(self._is16, 0, own))
-        rec["grad"] = self._ptrs(grads)
-        rec["gt"] = [_DTYPE[g.dtype] for g in grads]
+    def _bind(self) -> None:
+        """The state's addresses in the tensors' records."""
+        rec, at = self._rec, self._starts
+        self._master_ptrs = at * np.uint64(4) + np.uint64(0 if self.master is None else self.master.data_ptr())
         size = np.uint64(4 if self.state_bits == 32 else 1)
         rec["m"] = at * size + np.uint64(self.exp_avg.data_ptr())
         rec["v"] = at * size + np.uint64(self.exp_avg_sq.data_ptr())
@@ -139,11 +145,21 @@ class AdamW:
             scale_at = at // np.uint64(BLOCK) * np.uint64(4)
             rec["m_scale"] = scale_at + np.uint64(self.exp_avg_scale.data_ptr())
             rec["v_scale"] = scale_at + np.uint64(self.exp_avg_sq_scale.data_ptr())
+
+    def _launch_here(self, step, grads, lr, grad_scale) -> None:
+        rec, dev = self._rec, step.get_device()
+        own = self._ptrs(self.params)  # a caller may have given a parameter other memory
+        rec["p16"] = own if self._all16 else np.where(self._is16, own, 0)
+        rec["p"] = self._master_ptrs if self._all_master else \
+            np.where(self._has_master, self._master_ptrs, np.where(self._is16, 0, own))
+        rec["grad"] = self._ptrs(grads)
         lr_dev = lr if isinstance(lr, torch.Tensor) else None
-        h = FtAdamwHyper(0.0 if lr_dev is not None else lr, *self.betas, self.eps)
+        h = _HYPER.pack(0.0 if lr_dev is not None else lr, *self.betas, self.eps)
         check("ft_adamw_step", load().ft_adamw_step(
-            rec.ctypes.data, len(rec), ctypes.byref(h), self.state_bits, step.data_ptr(),
-            _f32(lr_dev, "lr", 1, dev), _f32(grad_scale, "grad_scale", 1, dev), _raw_stream(step)))
+            self._rec_addr, len(rec), h, self.state_bits, step.data_ptr(), _f32(lr_dev, "lr", 1, dev),
+            _f32(grad_scale, "grad_scale", 1, dev), _raw_stream(dev)))
+
+    _launch = _on_device(1)(_launch_here)
 
     def state_values(self):
         """(first, second) moments as flat float32 tensors: the state itself

@@ -27,7 +27,7 @@ from dataclasses import dataclass
 
 import torch
 
-from . import (BF16, Layer, Workspace, ft_linear_bwd, ft_linear_fwd, ft_set_cooperative_quantizer,
+from . import (BF16, AdamW, Layer, Workspace, ft_linear_bwd, ft_linear_fwd, ft_set_cooperative_quantizer,
                ft_workspace_bytes)
 
 
@@ -80,8 +80,15 @@ class LinearStack:
         ft_linear_bwd(self.layers[j], dY, X, b.P, amax_dy=amax, out_dtype=self.out_dtype, dX=b.dX, dA=b.dA,
                       dB=b.dB, ws=self.ws)
 
+    def optimizer(self, **kw) -> AdamW:
+        """AdamW on the adapters of all layers, reading the gradients that
+        step() leaves; keywords as AdamW's (lr, betas, state_bits, ...).  The
+        layers read the stepped adapters from their next call on."""
+        pairs = [p for L, b in zip(self.layers, self.bufs) if L.r_l > 0 for p in ((L.A, b.dA), (L.B, b.dB))]
+        return AdamW([p for p, _ in pairs], [g for _, g in pairs], **kw)
+
     def step(self, Xs: list[torch.Tensor], dYs: list[torch.Tensor], group=None, x_ready=None,
-             dy_ready=None) -> None:
+             dy_ready=None, optimizer: AdamW | None = None, grad_scale: torch.Tensor | None = None) -> None:
         """Forward of every layer in order, then backward in reverse order.
         With a process group of more than one rank, each layer's adapter
         gradients are summed over the ranks by an all-reduce started right
@@ -89,7 +96,9 @@ class LinearStack:
         been made to wait for all of them.  x_ready / dy_ready: optional
         CUDA events, one per layer, that the layer's forward / backward
         waits for first (inputs arriving on another stream, e.g. host copies
-        overlapped with the layers before)."""
+        overlapped with the layers before).  optimizer: steps the adapters
+        once the exchanges are in, on gradients times grad_scale (a float32
+        device scalar; 1 / ranks makes the sum over ranks their mean)."""
         import torch.distributed as dist
         exchange = dist.is_initialized() and dist.get_world_size(group) > 1
         stream = torch.cuda.current_stream() if (x_ready is not None or dy_ready is not None) else None
@@ -113,3 +122,5 @@ class LinearStack:
                 ft_set_cooperative_quantizer(False)
         for h in handles:
             h.wait()
+        if optimizer is not None:
+            optimizer.step(grad_scale=grad_scale)

@@ -28,6 +28,29 @@ def test_struct_sizes():
     assert ctypes.sizeof(FtAdamwHyper) == 32
 
 
+def test_packed_structs_are_the_declared_ones():
+    """The binding packs a call's structs with the struct module: same size
+    and, field by field, the same offsets as the declarations."""
+    import struct
+    from bit_quantized_lora_b200 import blockops, optim
+    for packed, declared in ((blockops._NORM, FtGatedNorm), (blockops._NORM_GRADS, FtGatedNormGrads),
+                             (blockops._ROPE, FtRope), (blockops._HEADS, FtHeads), (optim._HYPER, FtAdamwHyper)):
+        assert packed.size == ctypes.sizeof(declared)
+        fmt = "".join(c * int(n or 1) for n, c in __import__("re").findall(r"(\d*)([qPifd])", packed.format))
+        at, offsets = 0, []
+        for c in fmt:
+            n = struct.calcsize("@" + c)
+            at = -(-at // n) * n
+            offsets.append(at)
+            at += n
+        want = []
+        for name, t in declared._fields_:
+            o = getattr(declared, name).offset
+            n = t._length_ if hasattr(t, "_length_") else 1
+            want += [o + k * ctypes.sizeof(t) // n for k in range(n)]
+        assert offsets == want
+
+
 def norm(**kw):
     d = dict(M=8, D=64, B=2, offsets=None, pre=2, post=0, eps_pre=1e-6, eps_post=1e-6, alpha=1.0, xt=0, pt=1,
              ld_gate=64, ld_scale=64, ld_shift=64, gate=P, scale=P, shift=P, w_post=None, w=None, bias=None)
