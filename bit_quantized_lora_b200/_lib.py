@@ -3,6 +3,8 @@ the CUDA library has not been built: there is no fallback implementation."""
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 from . import build as _build
@@ -96,7 +98,7 @@ class FtRope(ctypes.Structure):
         ("layout", ctypes.c_int32),
         ("norm", ctypes.c_int32),
         ("eps", ctypes.c_float),
-        ("post", ctypes.c_int32),
+        ("pos_t", ctypes.c_int32),
         ("pt", ctypes.c_int32),
         ("pos", c_vp),
         ("freqs", c_vp),
@@ -216,6 +218,25 @@ def load(build_if_missing: bool = True):
         fn.argtypes = args
     _lib = L
     return L
+
+
+_torch_side = None
+
+
+def load_torch():
+    """The C++ side of the operators that take torch tensors (csrc/ft_torch.cpp),
+    built with the CUDA library and linked to it."""
+    global _torch_side
+    if _torch_side is None:
+        load()
+        if _build.needs_build_torch():
+            _build.build_torch()
+        loader = importlib.machinery.ExtensionFileLoader("_ft_torch", _build.TORCH_LIB)
+        spec = importlib.util.spec_from_file_location("_ft_torch", _build.TORCH_LIB, loader=loader)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+        _torch_side = module
+    return _torch_side
 
 
 class FtError(RuntimeError):

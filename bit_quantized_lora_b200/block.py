@@ -52,7 +52,8 @@ class DitBlock:
     [M, axes].  attention.forward(q, k, v) takes [samples, heads, tokens,
     head_dim] and returns (o of q's shape, what its backward needs);
     attention.backward(do, saved) returns (dq, dk, dv).  Returns (x', saved).
-    backward(dx', saved, attention) returns BlockGrads."""
+    backward(dx', saved, attention) returns BlockGrads.  A block's calls share
+    its workspace and go to one stream at a time."""
 
     def __init__(self, qkv: Layer, out: Layer, up: Layer, down: Layer, rope: Rope, norm: int = NORM_LAYER,
                  eps: float = 1e-6):
@@ -77,7 +78,7 @@ class DitBlock:
     def forward(self, x: torch.Tensor, mod: torch.Tensor, pos: torch.Tensor, attention):
         M, D = x.shape
         B = len(mod)
-        if mod.shape != (B, 6, D) or B < 1 or M % B:
+        if mod.shape != (B, 6, D) or B < 1 or M < 1 or M % B:
             raise ValueError(f"mod must be [samples, 6, {D}] with samples that divide the {M} rows of x")
         ws = self._workspace(M, x.device)
         amax = x.new_zeros(2, dtype=torch.float32)
@@ -85,7 +86,7 @@ class DitBlock:
         y_qkv, p_qkv = ft_linear_fwd(self.qkv, h1, amax_x=amax[:1], ws=ws)
         q, k, v = ft_qk_rope_fwd(self.rope, y_qkv, pos, tokens=M // B)
         o, saved_attn = attention.forward(q, k, v)
-        o = o.transpose(1, 2).reshape(M, -1)
+        o = o.transpose(1, 2).reshape(M, self.out.K)
         y_out, p_out = ft_linear_fwd(self.out, o, ws=ws)
         r, h2, st2 = ft_gated_norm_fwd(self.norm, x, y_out, mod[:, GATE1], mod[:, SCALE2], mod[:, SHIFT2],
                                        amax_h=amax[1:])

@@ -1,4 +1,5 @@
-"""Builds libft_b200.so, the sm_100a CUDA library behind include/ft.h.
+"""Builds libft_b200.so, the sm_100a CUDA library behind include/ft.h, and
+_ft_torch.so, the torch side of the operators around the linears.
 
     python -m bit_quantized_lora_b200.build
 
@@ -16,6 +17,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 SRC_DIR = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libft_b200.so")
+TORCH_SRC = os.path.join(SRC_DIR, "ft_torch.cpp")
+TORCH_LIB = os.path.join(OUT_DIR, "_ft_torch.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "ft.h")
 
 NVCC_FLAGS = [
@@ -55,5 +58,39 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB
 
 
+def needs_build_torch() -> bool:
+    if not os.path.exists(TORCH_LIB):
+        return True
+    t = os.path.getmtime(TORCH_LIB)
+    return any(os.path.getmtime(s) > t for s in (TORCH_SRC, HEADER))
+
+
+def build_torch(force: bool = False) -> str:
+    """The operators' torch side: host C++ against torch's headers, linked to
+    the CUDA library beside it."""
+    if not force and not needs_build_torch():
+        return TORCH_LIB
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    tmp = TORCH_LIB + f".tmp{os.getpid()}"
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *("-isystem" + p for p in include), TORCH_SRC, "-o", tmp,
+           "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_python",
+           "-L" + OUT_DIR, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        sys.stderr.write(res.stdout + res.stderr)
+        raise RuntimeError("the C++ compiler failed building _ft_torch.so")
+    os.replace(tmp, TORCH_LIB)
+    return TORCH_LIB
+
+
 if __name__ == "__main__":
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))
+    print(build_torch(force="--force" in sys.argv))

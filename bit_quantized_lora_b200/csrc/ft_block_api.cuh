@@ -93,17 +93,21 @@ uint32_t norm_has(const ft_gated_norm* n) {
 // Blocks of `k` that an SM holds; lets the kernel take its shared memory
 // first.  Asked once per kernel and launch shape in a context.
 ft_status blocks_per_sm(const void* k, int threads, size_t smem, DevInfo* d, int* out) {
-    std::lock_guard<std::mutex> lk(g_mu);
-    int& n = d->per_sm[std::make_tuple(k, threads, smem)];
-    if (n == 0) {
-        int got = 0;
-        if (smem > 32 * 1024)  // with the static part, above what a launch may take unasked
-            FT_TRY(cuda_ok(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)));
-        FT_TRY(cuda_ok(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&got, k, threads, smem)));
-        n = std::max(1, got);
+    try {
+        std::lock_guard<std::mutex> lk(g_mu);
+        int& n = d->per_sm[std::make_tuple(k, threads, smem)];
+        if (n == 0) {
+            int got = 0;
+            if (smem > 32 * 1024)  // with the static part, above what a launch may take unasked
+                FT_TRY(cuda_ok(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)));
+            FT_TRY(cuda_ok(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&got, k, threads, smem)));
+            n = std::max(1, got);
+        }
+        *out = n;
+        return FT_OK;
+    } catch (...) {  // no memory for the entry: nothing may leave a C entry point
+        return FT_ERR_CUDA;
     }
-    *out = n;
-    return FT_OK;
 }
 // Launches `k` with `smem` bytes of dynamic shared memory per block, the grid
 // cut to the blocks that the device holds at once when `resident` is set.
@@ -171,7 +175,7 @@ ft_status check_rope(const ft_rope* R) {
         return FT_ERR_INVALID_ARG;
     if (R->layout != FT_ROPE_PAIRS && R->layout != FT_ROPE_HALVES) return FT_ERR_INVALID_ARG;
     if (R->norm != FT_NORM_NONE && R->norm != FT_NORM_RMS) return FT_ERR_INVALID_ARG;
-    if (R->post != FT_POS_I32 && R->post != FT_POS_F32) return FT_ERR_INVALID_ARG;
+    if (R->pos_t != FT_POS_I32 && R->pos_t != FT_POS_F32) return FT_ERR_INVALID_ARG;
     if (!dtype_ok(R->pt) || !(R->eps >= 0.0f)) return FT_ERR_INVALID_ARG;
     if ((R->w_q || R->w_k) && R->norm == FT_NORM_NONE) return FT_ERR_INVALID_ARG;
     if (R->hd < 8 || R->hd % 8 || R->hd > 256 || R->Hq > 65536 || R->Hk > 65536) return FT_ERR_SHAPE;
@@ -209,7 +213,7 @@ ft::rope::Params rope_params(const ft_rope* R, const ft_heads* q, const ft_heads
     p.Hv = v->p ? R->Hk : 0;
     p.halves = R->layout == FT_ROPE_HALVES;
     p.norm = R->norm != FT_NORM_NONE;
-    p.pos_f32 = R->post == FT_POS_F32;
+    p.pos_f32 = R->pos_t == FT_POS_F32;
     p.p32 = R->pt == FT_F32;
     p.n_axes = R->n_axes;
     for (int a = 0, end = 0; a < R->n_axes; ++a) {
@@ -291,8 +295,9 @@ ft_status adamw_group(const ft_adamw_tensor* t, int64_t begin, int64_t end, cons
     p.grad_scale = grad_scale;
     p.step = reinterpret_cast<long long*>(step);
     p.last = last;
-    // 1e-18 is more than the square root of any subnormal v / (1 - beta2^t)
-    p.exact = !(h->eps >= 1e-16);
+    // The fast root leaves out what a subnormal v adds to eps, at most
+    // 1.1e-19 / sqrt(1 - beta2): below 2^-21 of eps it does not count.
+    p.exact = !(h->eps * std::sqrt(1.0 - h->beta2) >= 2.5e-13);
     for (int64_t i = begin; i < end; ++i) {
         const ft_adamw_tensor& a = t[i];
         if (a.n == 0) continue;

@@ -14,13 +14,25 @@ import numpy as np
 import torch
 
 from ._lib import FtAdamwTensor, check, load
-from .blockops import _DTYPE, _f32, _on_device, _raw_stream
+from .blockops import _on_device
 
+_DTYPE = {torch.bfloat16: 0, torch.float32: 1}
+_raw_stream = torch._C._cuda_getCurrentRawStream
 BLOCK = 256  # consecutive values that share a scale of an 8-bit state
 _RECORD = np.dtype([("p", "u8"), ("p16", "u8"), ("grad", "u8"), ("m", "u8"), ("v", "u8"), ("m_scale", "u8"),
                     ("v_scale", "u8"), ("n", "i8"), ("weight_decay", "f4"), ("gt", "i4")])
 _HYPER = struct.Struct("@4d")  # ft_adamw_hyper
 assert _RECORD.itemsize == ctypes.sizeof(FtAdamwTensor)
+
+
+def _f32(t, name: str, n: int, dev: int):
+    if t is None:
+        return None
+    if t.dtype is not torch.float32 or t.numel() < n or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous float32 tensor of {n}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the call is on cuda:{dev}")
+    return t.data_ptr()
 
 
 @_on_device(0)
@@ -66,6 +78,9 @@ class AdamW:
                 raise TypeError("parameters must be CUDA bfloat16 or float32 tensors")
             if not p.is_contiguous() or p.device != dev:
                 raise ValueError("parameters must be contiguous and on one device")
+        used = [p.data_ptr() for p in self.params if p.numel()]
+        if len(set(used)) < len(used):
+            raise ValueError("a parameter is listed twice")
         self.lr, self.betas, self.eps, self.state_bits = lr, tuple(betas), eps, state_bits
         decay = [float(weight_decay)] * len(self.params) if np.isscalar(weight_decay) else list(weight_decay)
         if len(decay) != len(self.params):

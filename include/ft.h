@@ -508,7 +508,7 @@ typedef enum { FT_ROPE_PAIRS = 0, FT_ROPE_HALVES = 1 } ft_rope_layout;
  *     <= hd; for FT_ROPE_HALVES a multiple of 8.  n_axes: 1 to 4.
  *   S : rows per sample of the outputs' layout (row m = token m % S of sample
  *     m / S); M a multiple of S.
- *   pos  : [M, n_axes] dense, of type post.
+ *   pos  : [M, n_axes] dense, of type pos_t.
  *   freqs: device FP64 [rot / 2], radians per position.
  *   norm : FT_NORM_NONE or FT_NORM_RMS (eps); w_q, w_k: its weights [hd], of
  *     type pt, or NULL (1).                                                */
@@ -519,7 +519,7 @@ typedef struct {
     int32_t layout; /* ft_rope_layout */
     int32_t norm;   /* ft_norm_kind */
     float eps;
-    int32_t post; /* ft_pos_dtype */
+    int32_t pos_t; /* ft_pos_dtype */
     int32_t pt;   /* ft_dtype */
     const void* pos;
     const double* freqs;
@@ -598,7 +598,8 @@ typedef struct {
  *   lr_dev   : NULL, or a device float used in place of lr (a captured step
  *              whose rate changes).
  *   grad_scale: NULL, or a device float (1 / ranks, a clipping factor).
- * Tensors with n = 0 are skipped; the step still counts.                   */
+ * Tensors with n = 0 are skipped; the step still counts.  A tensor is listed
+ * once.                                                                    */
 typedef struct {
     double lr, beta1, beta2, eps;
 } ft_adamw_hyper;

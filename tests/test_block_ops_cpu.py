@@ -28,27 +28,32 @@ def test_struct_sizes():
     assert ctypes.sizeof(FtAdamwHyper) == 32
 
 
-def test_packed_structs_are_the_declared_ones():
-    """The binding packs a call's structs with the struct module: same size
-    and, field by field, the same offsets as the declarations."""
-    import struct
-    from bit_quantized_lora_b200 import blockops, optim
-    for packed, declared in ((blockops._NORM, FtGatedNorm), (blockops._NORM_GRADS, FtGatedNormGrads),
-                             (blockops._ROPE, FtRope), (blockops._HEADS, FtHeads), (optim._HYPER, FtAdamwHyper)):
-        assert packed.size == ctypes.sizeof(declared)
-        fmt = "".join(c * int(n or 1) for n, c in __import__("re").findall(r"(\d*)([qPifd])", packed.format))
-        at, offsets = 0, []
-        for c in fmt:
-            n = struct.calcsize("@" + c)
-            at = -(-at // n) * n
-            offsets.append(at)
-            at += n
-        want = []
-        for name, t in declared._fields_:
-            o = getattr(declared, name).offset
-            n = t._length_ if hasattr(t, "_length_") else 1
-            want += [o + k * ctypes.sizeof(t) // n for k in range(n)]
-        assert offsets == want
+def test_the_torch_side_loads():
+    m = _lib.load_torch()
+    for name in ("gated_norm_fwd", "gated_norm_bwd", "gelu_bwd", "qk_rope_fwd", "qk_rope_bwd"):
+        assert callable(getattr(m, name))
+    from bit_quantized_lora_b200 import optim
+    assert optim._HYPER.size == ctypes.sizeof(FtAdamwHyper)
+
+
+def test_the_torch_side_says_what_is_wrong():
+    """Refusals that name shapes and types, before any device is asked."""
+    import bit_quantized_lora_b200 as ft
+    m, x, z = _lib.load_torch(), torch.zeros(4, 64), torch.zeros
+
+    def call(norm=ft.GatedNorm(), x=x, gate=None, scale=None, offsets=None):
+        return m.gated_norm_fwd(norm, x, None, gate, scale, None, offsets, None, None, True, None)
+
+    for error, text, kw in ((ValueError, r"gate must be \[3, 64\] or \[64\], not \[3, 5\]", dict(gate=z(3, 5))),
+                            (ValueError, r"not \[2, 2, 2\]", dict(scale=z(2, 2, 2))),
+                            (ValueError, r"weight must be contiguous \[64\], not \[3\]",
+                             dict(norm=ft.GatedNorm(weight=z(3)))),
+                            (ValueError, r"x must be \[rows, channels\]", dict(x=x[0])),
+                            (TypeError, "bfloat16 or float32", dict(x=x.half())),
+                            (TypeError, "int32", dict(offsets=z(2))),
+                            (ValueError, "cpu", dict())):
+        with pytest.raises(error, match=text):
+            call(**kw)
 
 
 def norm(**kw):
@@ -142,7 +147,7 @@ def test_gelu_backward_refusals(L):
 
 def rope(**kw):
     d = dict(M=4, S=2, Hq=4, Hk=2, hd=64, n_axes=2, axis_dims=(ctypes.c_int32 * 4)(16, 32, 0, 0), layout=0, norm=1,
-             eps=1e-6, post=0, pt=1, pos=P, freqs=P, w_q=P, w_k=P)
+             eps=1e-6, pos_t=0, pt=1, pos=P, freqs=P, w_q=P, w_k=P)
     if "axis_dims" in kw:
         kw["axis_dims"] = (ctypes.c_int32 * 4)(*kw["axis_dims"])
     d.update(kw)
@@ -163,7 +168,7 @@ def rope_fwd(L, r, x=P, ld=512, q=None, k=None, v=None):
 def test_rope_refusals(L):
     h = heads()
     assert L.ft_qk_rope_fwd(None, P, 512, ctypes.byref(h), ctypes.byref(h), ctypes.byref(h), None) == ARG
-    for bad in (dict(M=-1), dict(Hq=-1), dict(n_axes=0), dict(n_axes=5), dict(layout=2), dict(norm=2), dict(post=2),
+    for bad in (dict(M=-1), dict(Hq=-1), dict(n_axes=0), dict(n_axes=5), dict(layout=2), dict(norm=2), dict(pos_t=2),
                 dict(pt=3), dict(eps=-1.0), dict(norm=0), dict(pos=None), dict(freqs=None)):
         assert rope_fwd(L, rope(**bad)) == ARG, bad
     for bad in (dict(hd=60), dict(hd=264), dict(hd=0), dict(axis_dims=(15, 32, 0, 0)), dict(axis_dims=(64, 32, 0, 0)),

@@ -231,6 +231,27 @@ def test_learning_rate_scale_and_gradients_of_the_call():
     assert torch.equal(a.exp_avg, b.exp_avg) and torch.equal(a.exp_avg_sq, b.exp_avg_sq)
 
 
+@pytest.mark.parametrize("eps,scale", [(0.0, 1e-3), (0.0, 1e-21), (1e-12, 1e-20), (1e-8, 1e-20), (1e-8, 1e15)])
+def test_eps_and_extreme_gradients(eps, scale):
+    """No eps at all, second moments that are subnormal or near the top of
+    FP32's range: still the formula (a subnormal keeps 2^-149 of spacing)."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    p = torch.randn(3000, generator=g, device="cuda")
+    p0 = p.clone()
+    grad = (1 + torch.rand(3000, generator=g, device="cuda")) * scale
+    opt = ft.AdamW([p], [grad], lr=2.0 ** -7, betas=(0.9, 0.999), eps=eps, weight_decay=0.0)
+    opt.step()
+    m, v = opt.exp_avg[:3000].double(), opt.exp_avg_sq[:3000].double()
+    gd = grad.double()
+    assert bool(((v - 0.001 * gd * gd).abs() <= 5 * R.U32 * 0.001 * gd * gd + 2.0 ** -148).all())
+    # the step from the moments as they are stored
+    upd = 2.0 ** -7 / 0.1 * m / ((v / 0.001).sqrt() + eps)
+    upd = torch.where(m == 0, torch.zeros_like(upd), upd)
+    fine = torch.isfinite(upd)
+    R.check_rounded(p[fine], (p0.double() - upd)[fine], 4 * R.U32 * p0[fine].double().abs() + 24 * R.U32 * upd[fine].abs())
+
+
 def test_state_is_saved_and_loaded():
     for bits in (32, 8):
         params, grads = make([3000, 10], seed=9)
@@ -301,6 +322,8 @@ def test_refusals():
         ft.AdamW(p, state_bits=16)
     with pytest.raises(ValueError):
         ft.AdamW(p, weight_decay=[0.1, 0.2])
+    with pytest.raises(ValueError):  # the same parameter twice
+        ft.AdamW([p[0], p[0]])
     o = ft.AdamW(p)
     with pytest.raises(ValueError):
         o.step([g[0][:32]])
