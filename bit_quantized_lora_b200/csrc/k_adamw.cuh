@@ -14,6 +14,8 @@
 // a captured step owns its list, and nothing is copied to the device first.
 #pragma once
 
+#include <type_traits>
+
 #include "../../include/ft.h"
 #include "ft_ptx.cuh"
 #include "ft_vec.cuh"
@@ -37,7 +39,7 @@ struct Tensor {
     long long n;
     float wd;
     unsigned first;  // units before this tensor
-    int g16, vec;
+    int g16, vec, usual;
 };
 template <int kMax>
 struct Params {
@@ -243,25 +245,27 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) k_adamw(const __grid_cons
         while (tensor + 1 < p.count && p.t[tensor + 1].first <= unit) ++tensor;
         const Tensor& T = p.t[tensor];
         const long long n = T.n;
-        const float decay = (float)(1.0 - lr * (double)T.wd);
-        const bool g16 = T.g16, aligned = T.vec;
-        float* const tp = T.p;
-        __nv_bfloat16* const tp16 = T.p16;
         const long long block = (long long)(unit - T.first) * kWarps + warp;
-        if (block * kBlock < n) {
-            const long long at = block * kBlock + lane * 4;
-            const int live = (int)max(0ll, min((long long)kBlock, n - at));  // of the block from this lane's first on
-            const bool vec = aligned && live >= kHalf + 4;
+        if (block * kBlock >= n) continue;
+        const long long at = block * kBlock + lane * 4;
+        const int live = (int)max(0ll, min((long long)kBlock, n - at));  // of the block from this lane's first on
+        const float decay = (float)(1.0 - lr * (double)T.wd);
+        // kUsual: FP32 masters with a bf16 copy and FP32 gradients, all there
+        // and aligned, known to the compiler
+        auto step = [&](auto usual) {
+            constexpr bool kUsual = decltype(usual)::value;
+            const bool vec = kUsual || (T.vec && live >= kHalf + 4);
+            const bool g16 = !kUsual && T.g16, has_p = kUsual || T.p, has_16 = kUsual || T.p16;
             float2 g[4], w[4], m[4], v[4];
             float mtop = 0.0f, vtop = 0.0f;
             if (g16)
                 load_pairs(g, static_cast<const __nv_bfloat16*>(T.g) + at, vec, live);
             else
                 load_pairs(g, static_cast<const float*>(T.g) + at, vec, live);
-            if (tp)
-                load_pairs(w, tp + at, vec, live);
+            if (has_p)
+                load_pairs(w, T.p + at, vec, live);
             else
-                load_pairs(w, tp16 + at, vec, live);
+                load_pairs(w, T.p16 + at, vec, live);
             if (k8) {
                 mtop = T.ms[block];
                 vtop = T.vs[block];
@@ -288,8 +292,8 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) k_adamw(const __grid_cons
                     u = make_float2(m[i].x / fmaf(sqrtf(v[i].x), rc2, p.eps), m[i].y / fmaf(sqrtf(v[i].y), rc2, p.eps));
                 w[i] = fma2(u, both(-rate), mul2(w[i], both(decay)));
             }
-            if (tp) store_pairs(tp + at, w, vec, live);
-            if (tp16) store_pairs(tp16 + at, w, vec, live);
+            if (has_p) store_pairs(T.p + at, w, vec, live);
+            if (has_16) store_pairs(T.p16 + at, w, vec, live);
             if (k8) {
                 // magnitudes order like their bits, NaN above infinity; what
                 // is not there is zero
@@ -317,7 +321,11 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) k_adamw(const __grid_cons
                 store_pairs(static_cast<float*>(T.m) + at, m, vec, live);
                 store_pairs(static_cast<float*>(T.v) + at, v, vec, live);
             }
-        }
+        };
+        if (T.usual && block * kBlock + kBlock <= n)  // uniform over the warp
+            step(std::true_type());
+        else
+            step(std::false_type());
     }
     // The last block to get here has seen every block read the count: it
     // counts the step and leaves the arrival word as it found it.

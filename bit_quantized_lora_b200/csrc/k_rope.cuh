@@ -59,7 +59,8 @@ struct Params {
     int rot, halves, norm, pos_f32, p32, n_axes;
     int axis_end[4];  // pairs up to and including axis a
     int lanes;        // per head
-    int slices;       // of a row's heads
+    int whole;        // rows that one warp takes each
+    int slices;       // of the heads of a row behind those
     float eps, inv_hd;
     const void* pos;
     const double* freqs;
@@ -235,16 +236,20 @@ __global__ void __maxnreg__((kRegs<kBwd, kNorm>)) k_qk_rope(const __grid_constan
     uint32_t amax = 0;
     const bool even = p.hd == 8 * lanes;  // every lane has values
     // A row's heads in turns of `groups`: queries, keys, values; a slice takes
-    // its share of the turns.  32 bits hold tasks and turns times slices: a
-    // row is sliced only when rows are few.
+    // its share of the turns.  32 bits hold tasks and turns times slices: only
+    // the rows of the last round are sliced.
     const int nq = (p.Hq + groups - 1) / groups, nk = (p.Hk + groups - 1) / groups, nv = (p.Hv + groups - 1) / groups;
     const int total = nq + nk + nv;
-    const uint32_t slices = p.slices, tasks = (uint32_t)p.M * slices, stride = gridDim.x * kWarps;
+    const uint32_t whole_rows = p.whole, slices = p.slices, stride = gridDim.x * kWarps;
+    const uint32_t tasks = whole_rows + ((uint32_t)p.M - whole_rows) * slices;
     for (uint32_t task = blockIdx.x * kWarps + warp; task < tasks; task += stride) {
-        const int m = slices == 1 ? (int)task : (int)(task / slices);
-        const uint32_t slice = task - m * slices;
-        const int from = slices == 1 ? 0 : (int)(total * slice / slices);
-        const int to = slices == 1 ? total : (int)(total * (slice + 1) / slices);
+        int m = (int)task, from = 0, to = total;
+        if (task >= whole_rows) {
+            const uint32_t part = task - whole_rows, row = part / slices, slice = part - row * slices;
+            m = (int)(whole_rows + row);
+            from = (int)(total * slice / slices);
+            to = (int)(total * (slice + 1) / slices);
+        }
         const int b = m / p.S, s = m - b * p.S;
         // this lane's values of its group's first head
         const __nv_bfloat16* x = p.x + (int64_t)m * p.ld + group * p.hd + lane.lo;
