@@ -232,10 +232,12 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) k_adamw(const __grid_cons
     const float gs = p.grad_scale ? *p.grad_scale : 1.0f;
     const double lr = p.lr_dev ? (double)*p.lr_dev : p.lr;
     if (threadIdx.x == 0) {
-        // 1 - b^t in FP64: it cancels for small t
+        // 1 - b^t by expm1, which does not cancel for small t; the exponent
+        // is formed in FP64 (FP64 expm1 too would hold every block back by
+        // 3 us)
         const double t = (double)(*p.step + 1);
-        coef[0] = (float)(lr / -expm1(t * p.log_b1));
-        coef[1] = (float)rsqrt(-expm1(t * p.log_b2));
+        coef[0] = (float)lr / -expm1f((float)(t * p.log_b1));
+        coef[1] = 1.0f / sqrtf(-expm1f((float)(t * p.log_b2)));
     }
     __syncthreads();
     const float rate = coef[0], rc2 = coef[1];

@@ -203,6 +203,9 @@ def test_shapes_and_kinds(shape, kind):
     dict(M=2000, D=64, B=9, weights=True, post=1, pre=1,
          offsets=[0, 1, 3, 300, 301, 700, 1400, 1401, 1999, 2000]),
     dict(M=700, D=2048, B=2, mean=50.0, xt=F32),                   # a mean far above the deviation
+    dict(M=4000, D=1536, B=3, offsets=[0, 1000, 1001, 4000]),      # many rows per block
+    dict(M=5001, D=128, B=1, pre=1),
+    dict(M=2400, D=4608, B=2, xt=F32, offsets=[0, 1300, 2400], pt=BF16),
 ], ids=lambda k: "-".join(f"{a}{v}" for a, v in k.items() if a != "offsets"))
 def test_samples_strides_and_absent_parts(kw):
     c = Case(seed=7, **kw)

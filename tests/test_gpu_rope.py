@@ -118,6 +118,8 @@ CASES = [
     dict(S=20, Hq=4, Hk=0, hd=64, axes=(32, 32), weights=False),
     dict(S=20, Hq=2, Hk=2, hd=64, axes=(0, 32)),
     dict(S=4, Hq=70, Hk=70, hd=128, axes=(128,)),
+    dict(S=2500, B=2, Hq=3, Hk=1, hd=64, axes=(32, 32)),             # more rows than the device holds warps
+    dict(S=9500, Hq=2, Hk=1, hd=40, axes=(16, 24), halves=True),
 ]
 
 
