@@ -291,6 +291,21 @@ def test_in_place():
     assert torch.equal(dr, out.dx) and torch.equal(dh, out.dy) and torch.equal(out2.dgate, out.dgate)
 
 
+@pytest.mark.parametrize("kw", [dict(M=300, D=1536), dict(M=70, D=96, post=2, weights=True)], ids=str)
+def test_in_place_of_the_block(kw):
+    """h over y, the stream over itself, and dy over y."""
+    c = Case(xt=BF16, **kw)
+    r, h, stats = c.forward()
+    want = c.backward(r, stats)
+    x, y = c.x, c.y
+    c.x, c.y = x.clone(), y.clone()
+    r2, h2, stats2 = c.forward(r=c.x, h=c.y)
+    assert torch.equal(c.x, r) and torch.equal(c.y, h) and torch.equal(stats2, stats)
+    c.y = y.clone()
+    got = c.backward(r2, stats, dy=c.y, dx=c.x)
+    assert torch.equal(c.y, want.dy) and torch.equal(c.x, want.dx) and torch.equal(got.dgate, want.dgate)
+
+
 def test_amax_is_raised_and_never_lowered():
     c = Case(40, 256)
     high = torch.full((1,), 1e6, device="cuda")

@@ -162,6 +162,19 @@ def test_strides_and_in_place():
     assert torch.equal(x[:, 6 * 64:], c.qkv[:, 6 * 64:])
 
 
+@pytest.mark.parametrize("norm", [True, False])
+def test_backward_in_place(norm):
+    """dq, dk and dv are the columns that dqkv is written to."""
+    c = Case(B=2, S=37, Hq=6, Hk=2, hd=64, norm=norm)
+    want, a, b = ft.ft_qk_rope_bwd(c.rope, c.d["q"], c.d["k"], c.d["v"], c.pos, qkv=c.qkv)
+    buf = torch.cat([c.rows(c.d[n]) for n in "qkv"], 1).reshape(c.M, c.width).contiguous()
+    parts = buf.view(c.B, c.S, -1, c.hd).transpose(1, 2)
+    got, a2, b2 = ft.ft_qk_rope_bwd(c.rope, parts[:, :6], parts[:, 6:8], parts[:, 8:], c.pos, qkv=c.qkv, dqkv=buf)
+    assert got.data_ptr() == buf.data_ptr() and torch.equal(buf, want)
+    if norm:
+        assert torch.equal(a, a2) and torch.equal(b, b2)
+
+
 def test_shared_frequencies_and_no_rows():
     axes = (8, 12, 12)
     f = ft.rope_freqs(axes, 500.0, shared=True)
