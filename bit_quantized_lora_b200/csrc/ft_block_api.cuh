@@ -606,7 +606,7 @@ ft_status ft_qk_rope_bwd(const ft_rope* R, const ft_heads* dq, const ft_heads* d
     }
     if (!dw) return FT_OK;
     LaunchTimer lt(KID_ROPE_REDUCE, st);
-    const ft_status e = launch_overlapped_args(ft::rope::k_qk_rope_reduce, cdiv(2 * R->hd, 32), 1024, 0, st,
+    const ft_status e = launch_overlapped_args(ft::rope::k_qk_rope_reduce, 2 * R->hd / 8, 1024, 0, st,
                                                static_cast<const float*>(ws), blocks, (int)R->hd, dw_q, dw_k);
     lt.stop();
     return e;
