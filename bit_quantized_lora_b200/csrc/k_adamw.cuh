@@ -12,8 +12,9 @@
 // written, g read, the bf16 copy written), 18 B with 8-bit ones.  The tensor
 // list travels in the launch's parameters, so one launch serves all tensors,
 // a captured step owns its list, and nothing is copied to the device first.
-// 24.5 M parameters in 64 tensors with 8-bit states take 86 us (0.78 of the
-// measured HBM rate), now bound by the 65 instructions of an element: IEEE
+// 24.5 M parameters in 64 tensors with 8-bit states take 86 us (a launch by
+// itself, which ends with 57 of its 441 MB still to leave L2; the floor is
+// 67.6), now bound by the 66 instructions of an element: IEEE
 // roots and divisions for every code took 132 us, and a lane's eight values
 // side by side (16-byte halves of the same sectors) instead of in two runs
 // made the decoding of a state 32 instead of 22 us.

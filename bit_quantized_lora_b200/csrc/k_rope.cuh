@@ -21,10 +21,10 @@
 // two-lane arithmetic in either layout.  HBM bounds both directions, 4 B per
 // element of qkv, 6 B per query and key element backward with a norm, as long
 // as a head's values cost few instructions: an SM moves three elements a
-// clock.  At 4608 rows of 3 x 24 heads of 128 with norms: 31 us forward (0.84
-// of the measured HBM rate) and 48 us backward (0.72);
-// a table of turns in shared memory that a block shares, with a lookup per
-// head, took 61 and 115 us.
+// clock.  At 4608 rows of 3 x 24 heads of 128 with norms, replayed back to back:
+// 36 us forward (0.73 of the measured HBM rate) and 52 us backward with the
+// weights' sums (0.67); a table of turns in shared memory that a block shares,
+// with a lookup per head, took 61 and 119 us.
 #pragma once
 
 #include <type_traits>
