@@ -50,6 +50,24 @@ def ft_adamw_decode(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor
     return out
 
 
+def _check_params(params, dev, dtypes=None, sizes=None) -> None:
+    """What a launch takes for granted of the parameters: where they lie, that
+    no two share memory, and (once chosen) their types and sizes."""
+    for i, p in enumerate(params):
+        if not p.is_cuda or p.dtype not in _DTYPE:
+            raise TypeError("parameters must be CUDA bfloat16 or float32 tensors")
+        if not p.is_contiguous() or p.device != dev:
+            raise ValueError("parameters must be contiguous and on one device")
+        if dtypes is not None and (p.dtype != dtypes[i] or p.numel() != sizes[i]):
+            raise ValueError("a parameter has another type or size than the optimizer was made for")
+    used = sorted((p.data_ptr(), p.nbytes) for p in params if p.numel())
+    for (a, n), (b, _) in zip(used, used[1:]):
+        if a == b:
+            raise ValueError("a parameter is listed twice")
+        if a + n > b:
+            raise ValueError("two parameters share memory")
+
+
 class AdamW:
     """AdamW on `params`, contiguous bf16 or float32 tensors of one device.
 
@@ -73,14 +91,9 @@ class AdamW:
         if not (0.0 <= betas[0] < 1.0 and 0.0 <= betas[1] < 1.0 and eps >= 0.0):
             raise ValueError("betas must lie in [0, 1) and eps must not be negative")
         dev = self.params[0].device
-        for p in self.params:
-            if not p.is_cuda or p.dtype not in _DTYPE:
-                raise TypeError("parameters must be CUDA bfloat16 or float32 tensors")
-            if not p.is_contiguous() or p.device != dev:
-                raise ValueError("parameters must be contiguous and on one device")
-        used = [p.data_ptr() for p in self.params if p.numel()]
-        if len(set(used)) < len(used):
-            raise ValueError("a parameter is listed twice")
+        _check_params(self.params, dev)
+        self._dtypes, self._sizes = [p.dtype for p in self.params], [p.numel() for p in self.params]
+        self._seen, self._seen_grads = self._memory(self.params), None
         self.lr, self.betas, self.eps, self.state_bits = lr, tuple(betas), eps, state_bits
         decay = [float(weight_decay)] * len(self.params) if np.isscalar(weight_decay) else list(weight_decay)
         if len(decay) != len(self.params):
@@ -129,6 +142,10 @@ class AdamW:
         self._rec["gt"] = [_DTYPE[g.dtype] for g in grads]
         return grads
 
+    @staticmethod
+    def _memory(ts) -> list:
+        return [(t.data_ptr(), t.nbytes) for t in ts]
+
     def step(self, grads=None, lr=None, grad_scale: torch.Tensor | None = None, stream=None) -> None:
         """One step from `grads` (or the optimizer's own).  lr: a float, or a
         float32 device scalar (a captured step whose rate changes), in place
@@ -138,11 +155,17 @@ class AdamW:
             grads = self._checked(grads)
         elif self.grads is not None:
             grads = self.grads
-            if self._lent:  # the last step read others
+            memory = self._memory(grads)
+            if self._lent or memory != self._seen_grads:  # the last step read others, or a caller exchanged one
                 self._checked(grads)
+                self._seen_grads = memory
         else:
             raise ValueError("step() needs gradients")
         self._lent = grads is not self.grads
+        memory = self._memory(self.params)
+        if memory != self._seen:  # a caller has given a parameter other memory
+            _check_params(self.params, self._step.device, self._dtypes, self._sizes)
+            self._seen = memory
         self._launch(self._step, grads, self.lr if lr is None else lr, grad_scale, stream=stream)
 
     @staticmethod
@@ -163,7 +186,7 @@ class AdamW:
 
     def _launch_here(self, step, grads, lr, grad_scale) -> None:
         rec, dev = self._rec, step.get_device()
-        own = self._ptrs(self.params)  # a caller may have given a parameter other memory
+        own = np.array([a for a, _ in self._seen], np.uint64)
         rec["p16"] = own if self._all16 else np.where(self._is16, own, 0)
         rec["p"] = self._master_ptrs if self._all_master else \
             np.where(self._has_master, self._master_ptrs, np.where(self._is16, 0, own))

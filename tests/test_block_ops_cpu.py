@@ -286,3 +286,43 @@ def test_python_side_refuses_cpu_tensors():
         ft.AdamW([x])
     with pytest.raises(ValueError):
         ft.AdamW([])
+
+
+class _Tensor:
+    """Stands in for a CUDA tensor where only its bookkeeping is looked at."""
+    is_cuda = True
+
+    def __init__(self, at, n, dtype=torch.float32, device="cuda:0", contiguous=True):
+        self.at, self.n, self.dtype, self.device, self.contiguous = at, n, dtype, device, contiguous
+        self.nbytes = n * dtype.itemsize
+
+    def data_ptr(self):
+        return self.at
+
+    def numel(self):
+        return self.n
+
+    def is_contiguous(self):
+        return self.contiguous
+
+
+def test_parameters_of_an_optimizer_are_apart_and_stay_what_they_were():
+    from bit_quantized_lora_b200.optim import _check_params
+    F, H = torch.float32, torch.bfloat16
+    ok = [_Tensor(4096, 64), _Tensor(4096 + 256, 64, H), _Tensor(0, 0)]
+    _check_params(ok, "cuda:0")
+    _check_params(ok, "cuda:0", [F, H, F], [64, 64, 0])
+    _check_params([_Tensor(9000, 64), _Tensor(0, 0), _Tensor(0, 0)], "cuda:0")  # empty ones lie nowhere
+    for bad, text in (
+            ([_Tensor(4096, 64), _Tensor(4096, 64)], "twice"),
+            ([_Tensor(4096, 64), _Tensor(4096 + 252, 64)], "share"),
+            ([_Tensor(8192, 64), _Tensor(8192 - 4, 2)], "share"),
+            ([_Tensor(4096, 64, device="cuda:1")], "one device"),
+            ([_Tensor(4096, 64, contiguous=False)], "contiguous")):
+        with pytest.raises(ValueError, match=text):
+            _check_params(bad, "cuda:0")
+    with pytest.raises(TypeError):
+        _check_params([_Tensor(4096, 64, torch.float16)], "cuda:0")
+    for now in (_Tensor(4096, 63), _Tensor(0, 0), _Tensor(4096, 64, H)):
+        with pytest.raises(ValueError, match="another type or size"):
+            _check_params([now], "cuda:0", [F], [64])

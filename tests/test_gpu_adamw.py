@@ -333,3 +333,38 @@ def test_refusals():
         o.step(g, lr=torch.zeros(1, dtype=torch.float64, device="cuda"))
     with pytest.raises(TypeError):
         ft.ft_adamw_decode(g[0], g[0])
+
+
+def test_exchanged_memory_is_looked_at_before_it_is_stepped():
+    """A parameter or gradient may move to other memory between steps; memory
+    of another size or type is refused, and nothing is stepped."""
+    sizes = [1000, 256]
+    params, grads = make(sizes, pdt=F32)
+    twin = [p.clone() for p in params]
+    opt, ref = ft.AdamW(params, grads), ft.AdamW(twin, [g.clone() for g in grads])
+    opt.step(), ref.step()
+    params[0].data = params[0].data.clone()
+    grads[1].data = grads[1].data.to(BF16).float()
+    ref.grads[1].copy_(grads[1])
+    opt.step(), ref.step()
+    for a, b in zip(params, twin):
+        assert torch.equal(a, b)
+    kept = params[0].data
+    for other in (kept[:10].clone(), kept.to(BF16), torch.empty(0, device="cuda"), kept.cpu()):
+        params[0].data = other
+        with pytest.raises((ValueError, TypeError)):
+            opt.step()
+    params[0].data = kept
+    held = grads[0].data
+    for other in (held[:10].clone(), torch.empty(0, device="cuda"), held.cpu()):
+        grads[0].data = other
+        with pytest.raises((ValueError, TypeError)):
+            opt.step()
+    grads[0].data = held
+    opt.step(), ref.step()
+    for a, b in zip(params, twin):
+        assert torch.equal(a, b)
+    assert int(opt.step_count) == 3
+    flat = torch.zeros(512, device="cuda")
+    with pytest.raises(ValueError):  # two that overlap
+        ft.AdamW([flat[:300], flat[256:]])
