@@ -79,7 +79,9 @@ class AdamW:
     place.  The state is flat, every parameter's part starting at a multiple
     of 256: master, exp_avg, exp_avg_sq (codes with 8-bit states) and
     exp_avg_scale, exp_avg_sq_scale; step_count is on the device, so a
-    captured step counts when it is replayed."""
+    captured step counts when it is replayed.  The state's tensors stay the
+    optimizer's own (a step holds their addresses): values are exchanged with
+    state_dict() and load_state_dict(), and the object is not copied."""
 
     def __init__(self, params, grads=None, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
                  weight_decay=0.01, state_bits: int = 32, master: bool = True):
@@ -161,6 +163,9 @@ class AdamW:
                 self._seen_grads = memory
         else:
             raise ValueError("step() needs gradients")
+        for mine, now in zip(self._held, self._state()):
+            if mine is not now:
+                raise ValueError("the state's tensors are the optimizer's own: load_state_dict() exchanges their values")
         self._lent = grads is not self.grads
         memory = self._memory(self.params)
         if memory != self._seen:  # a caller has given a parameter other memory
@@ -183,6 +188,14 @@ class AdamW:
             scale_at = at // np.uint64(BLOCK) * np.uint64(4)
             rec["m_scale"] = scale_at + np.uint64(self.exp_avg_scale.data_ptr())
             rec["v_scale"] = scale_at + np.uint64(self.exp_avg_sq_scale.data_ptr())
+        self._held = self._state()
+
+    def _state(self) -> tuple:
+        return (self.master, self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale)
+
+    def __reduce_ex__(self, protocol):
+        # copies and pickles would carry this object's addresses
+        raise TypeError("an AdamW is not copied: make another and load its state_dict()")
 
     def _launch_here(self, step, grads, lr, grad_scale) -> None:
         rec, dev = self._rec, step.get_device()

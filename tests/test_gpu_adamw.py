@@ -5,6 +5,9 @@ Tolerances of the 32-bit step: m takes three roundings, v four, each 2^-24 of
 the magnitudes that meet; the update lr m / (sqrt(v) rc + eps) at most 16
 more, and the parameter two.
 """
+import copy
+import pickle
+
 import numpy as np
 import pytest
 import torch
@@ -368,3 +371,21 @@ def test_exchanged_memory_is_looked_at_before_it_is_stepped():
     flat = torch.zeros(512, device="cuda")
     with pytest.raises(ValueError):  # two that overlap
         ft.AdamW([flat[:300], flat[256:]])
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_an_optimizer_is_not_copied_and_keeps_its_state(bits):
+    params, grads = make([300])
+    opt = ft.AdamW(params, grads, state_bits=bits)
+    for copied in (copy.copy, copy.deepcopy, pickle.dumps):
+        with pytest.raises(TypeError, match="state_dict"):
+            copied(opt)
+    for name in ("master", "exp_avg", "exp_avg_sq") + (("exp_avg_scale", "exp_avg_sq_scale") if bits == 8 else ()):
+        mine = getattr(opt, name)
+        setattr(opt, name, mine.clone())
+        with pytest.raises(ValueError, match="load_state_dict"):
+            opt.step()
+        setattr(opt, name, mine)
+    assert int(opt.step_count) == 0
+    opt.step()
+    assert int(opt.step_count) == 1
