@@ -25,9 +25,14 @@ def _on_device(at: int):
     """Runs a call with its tensors' device and the stream it was given (or
     that device's current one) current; argument `at` is such a tensor."""
     def wrap(fn):
+        name = fn.__code__.co_varnames[at]
+
         @functools.wraps(fn)
         def call(*args, stream=None, **kw):
-            dev = args[at].get_device()
+            some = args[at] if len(args) > at else kw.get(name)
+            if not isinstance(some, torch.Tensor):
+                raise TypeError(f"{fn.__name__} needs CUDA tensors")
+            dev = some.get_device()
             if dev < 0:
                 raise TypeError(f"{fn.__name__} needs CUDA tensors")
             if stream is None and dev == torch._C._cuda_getDevice():

@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import block_ref as R
+import bit_quantized_lora_b200 as ft
 from bit_quantized_lora_b200 import _lib
 from bit_quantized_lora_b200._lib import (FtAdamwHyper, FtAdamwTensor, FtGatedNorm, FtGatedNormGrads, FtHeads, FtRope)
 
@@ -326,3 +327,17 @@ def test_parameters_of_an_optimizer_are_apart_and_stay_what_they_were():
     for now in (_Tensor(4096, 63), _Tensor(0, 0), _Tensor(4096, 64, H)):
         with pytest.raises(ValueError, match="another type or size"):
             _check_params([now], "cuda:0", [F], [64])
+
+
+def test_calls_by_position_and_by_name_refuse_alike():
+    x, n = torch.zeros(2, 16, dtype=torch.bfloat16), ft.GatedNorm()
+    rope = ft.Rope(heads=1, kv_heads=0, head_dim=16, axes=(16,), freqs=torch.zeros(8, dtype=torch.float64))
+    pos = torch.zeros(2, dtype=torch.int32)
+    for call in (lambda: ft.ft_gated_norm_fwd(n, x), lambda: ft.ft_gated_norm_fwd(norm=n, x=x),
+                 lambda: ft.ft_gated_norm_fwd(n), lambda: ft.ft_gated_norm_fwd(n, None),
+                 lambda: ft.ft_gated_norm_bwd(norm=n, dh=x, r=x, stats=x),
+                 lambda: ft.ft_gelu_bwd_bf16(x, x), lambda: ft.ft_gelu_bwd_bf16(y=x, dh=x),
+                 lambda: ft.ft_qk_rope_fwd(rope, x, pos), lambda: ft.ft_qk_rope_fwd(rope=rope, qkv=x, pos=pos),
+                 lambda: ft.ft_adamw_decode(x, x), lambda: ft.ft_adamw_decode(codes=x, scales=x)):
+        with pytest.raises(TypeError, match="CUDA"):
+            call()
