@@ -95,7 +95,6 @@ class AdamW:
         dev = self.params[0].device
         _check_params(self.params, dev)
         self._dtypes, self._sizes = [p.dtype for p in self.params], [p.numel() for p in self.params]
-        self._seen, self._seen_grads = self._memory(self.params), None
         self.lr, self.betas, self.eps, self.state_bits = lr, tuple(betas), eps, state_bits
         decay = [float(weight_decay)] * len(self.params) if np.isscalar(weight_decay) else list(weight_decay)
         if len(decay) != len(self.params):
@@ -119,7 +118,7 @@ class AdamW:
                     self.master[s * BLOCK:s * BLOCK + p.numel()].copy_(p.detach().reshape(-1))
         self._step = torch.zeros(2, dtype=torch.int64, device=dev)
         self.step_count = self._step[:1]
-        # the tensors' records; addresses that a caller can change are read anew by each step
+        # the tensors' records; a step looks whether a caller has exchanged memory and writes the new addresses
         self._starts = starts.astype(np.uint64) * np.uint64(BLOCK)
         self._has_master = np.array(has_master)
         self._is16 = np.array([p.dtype == torch.bfloat16 for p in self.params])
@@ -127,9 +126,9 @@ class AdamW:
         self._rec["n"] = [p.numel() for p in self.params]
         self._rec["weight_decay"] = decay
         self._rec_addr = self._rec.ctypes.data
-        self._all16, self._all_master = bool(self._is16.all()), bool(self._has_master.all())
         self._bind()
-        self._lent = False
+        self._bind_params(self._memory(self.params))
+        self._lent, self._seen_grads = True, None  # the records hold no gradients of the optimizer's own yet
         self.grads = None if grads is None else self._checked(grads)
 
     def _checked(self, grads) -> list:
@@ -154,28 +153,35 @@ class AdamW:
         of the optimizer's.  grad_scale: a float32 device scalar that
         multiplies the gradients (1 / ranks, a clipping factor)."""
         if grads is not None:
-            grads = self._checked(grads)
-        elif self.grads is not None:
-            grads = self.grads
-            memory = self._memory(grads)
-            if self._lent or memory != self._seen_grads:  # the last step read others, or a caller exchanged one
-                self._checked(grads)
-                self._seen_grads = memory
-        else:
+            self._lend(grads)
+        elif self.grads is None:
             raise ValueError("step() needs gradients")
-        for mine, now in zip(self._held, self._state()):
-            if mine is not now:
-                raise ValueError("the state's tensors are the optimizer's own: load_state_dict() exchanges their values")
-        self._lent = grads is not self.grads
+        else:
+            memory = self._memory(self.grads)
+            if self._lent or memory != self._seen_grads:  # the last step read others, or a caller exchanged one
+                self._lend(self.grads)
+                self._seen_grads, self._lent = memory, False
+        held = self._held
+        if not (held[0] is self.master and held[1] is self.exp_avg and held[2] is self.exp_avg_sq and
+                held[3] is self.exp_avg_scale and held[4] is self.exp_avg_sq_scale):
+            raise ValueError("the state's tensors are the optimizer's own: load_state_dict() exchanges their values")
         memory = self._memory(self.params)
         if memory != self._seen:  # a caller has given a parameter other memory
             _check_params(self.params, self._step.device, self._dtypes, self._sizes)
-            self._seen = memory
-        self._launch(self._step, grads, self.lr if lr is None else lr, grad_scale, stream=stream)
+            self._bind_params(memory)
+        self._launch(self._step, self.lr if lr is None else lr, grad_scale, stream=stream)
 
-    @staticmethod
-    def _ptrs(ts) -> np.ndarray:
-        return np.array([t.data_ptr() for t in ts], np.uint64)
+    def _lend(self, grads) -> None:
+        """The gradients' addresses in the tensors' records."""
+        self._lent = True
+        self._rec["grad"] = [t.data_ptr() for t in self._checked(grads)]
+
+    def _bind_params(self, memory) -> None:
+        """The parameters' addresses in the tensors' records."""
+        rec, own = self._rec, np.array([a for a, _ in memory], np.uint64)
+        rec["p16"] = np.where(self._is16, own, 0)
+        rec["p"] = np.where(self._has_master, self._master_ptrs, np.where(self._is16, 0, own))
+        self._seen = memory
 
     def _bind(self) -> None:
         """The state's addresses in the tensors' records."""
@@ -197,17 +203,12 @@ class AdamW:
         # copies and pickles would carry this object's addresses
         raise TypeError("an AdamW is not copied: make another and load its state_dict()")
 
-    def _launch_here(self, step, grads, lr, grad_scale) -> None:
-        rec, dev = self._rec, step.get_device()
-        own = np.array([a for a, _ in self._seen], np.uint64)
-        rec["p16"] = own if self._all16 else np.where(self._is16, own, 0)
-        rec["p"] = self._master_ptrs if self._all_master else \
-            np.where(self._has_master, self._master_ptrs, np.where(self._is16, 0, own))
-        rec["grad"] = self._ptrs(grads)
+    def _launch_here(self, step, lr, grad_scale) -> None:
+        dev = step.get_device()
         lr_dev = lr if isinstance(lr, torch.Tensor) else None
         h = _HYPER.pack(0.0 if lr_dev is not None else lr, *self.betas, self.eps)
         check("ft_adamw_step", load().ft_adamw_step(
-            self._rec_addr, len(rec), h, self.state_bits, step.data_ptr(), _f32(lr_dev, "lr", 1, dev),
+            self._rec_addr, len(self._rec), h, self.state_bits, step.data_ptr(), _f32(lr_dev, "lr", 1, dev),
             _f32(grad_scale, "grad_scale", 1, dev), _raw_stream(dev)))
 
     _launch = _on_device(1)(_launch_here)

@@ -389,3 +389,19 @@ def test_an_optimizer_is_not_copied_and_keeps_its_state(bits):
     assert int(opt.step_count) == 0
     opt.step()
     assert int(opt.step_count) == 1
+
+
+def test_a_refused_step_on_lent_gradients_leaves_no_trace():
+    params, grads = make([700, 40])
+    twin = [p.clone() for p in params]
+    opt, ref = ft.AdamW(params, grads), ft.AdamW(twin, grads)
+    opt.step(), ref.step()
+    mine, opt.exp_avg = opt.exp_avg, opt.exp_avg.clone()
+    with pytest.raises(ValueError):
+        opt.step([g.clone().fill_(1.0) for g in grads])
+    opt.exp_avg = mine
+    opt.step(), ref.step()
+    others = [g * 3 for g in grads]
+    opt.step(others), ref.step(iter(others))
+    opt.step(), ref.step()
+    assert all(torch.equal(a, b) for a, b in zip(params, twin)) and int(opt.step_count) == 4
