@@ -351,12 +351,23 @@ constexpr int LG_MAX_SPLITS = 16;
 static_assert(QD_MAX_SPLITS <= ft::qres::MAX_SPLITS, "k_qres reduces at most MAX_SPLITS partials");
 static_assert(LG_MAX_SPLITS <= ft::lgrad::MAX_SPLITS, "k_lora_grad reduces at most MAX_SPLITS partials");
 
+// The epoch-tagged words: what they hold must come from earlier calls (or be
+// zero), so everything else that is kept in a workspace, the scratch of the
+// operators around the linears included, lies behind these bytes.
+constexpr size_t kWsSyncBytes = 256;
+constexpr size_t kWsQcntBytes = (size_t)QRES_MAX_ROW_TILES * 8;
+constexpr size_t kWsLgcntBytes = (size_t)2 * LG_MAX_CTILES * 8;
+constexpr size_t kWsAmaxBytes = 256;
+constexpr size_t kWsWords = kWsSyncBytes + kWsQcntBytes + kWsLgcntBytes + kWsAmaxBytes;
+static_assert(kWsWords % 256 == 0, "what follows the words is aligned");
+
 struct WsPlan {
     size_t amax, gact, codes, scales, sfslab, lt, part, pg, lgpart, sync, qcnt, lgcnt, counters, total;
     int n_qd_counters, lg_ctiles;
     // sync: the resident quantizer's epoch-tagged words (grid-barrier
     // arrivals, tensor amax, finished CTAs); qcnt: its row-tile counters;
-    // lgcnt: the adapter-gradient tile counters (all epoch-tagged: no reset);
+    // lgcnt: the adapter-gradient tile counters; amax: the amax pass's word
+    // (all epoch-tagged: no reset);
     // counters: the streaming quantizer's row-tile counters (zeroed per call)
 };
 
@@ -384,14 +395,14 @@ WsPlan plan_ws(int64_t M, int64_t N, int64_t K, int64_t r_s, int64_t r_l) {
     WsPlan w;
     const int64_t C = std::max(N, K);
     const int64_t r = r_s + r_l;
-    size_t o = 0;
     // The epoch-tagged words come first, at offsets no shape changes, so a
     // workspace shared by calls of different shapes only ever holds epoch
     // counters there (their content from any earlier call is valid).
-    w.sync = o;   o += 256;
-    w.qcnt = o;   o += (size_t)QRES_MAX_ROW_TILES * 8;
-    w.lgcnt = o;  o += (size_t)2 * LG_MAX_CTILES * 8;
-    w.amax = o;   o += 256;
+    w.sync = 0;
+    w.qcnt = w.sync + kWsSyncBytes;
+    w.lgcnt = w.qcnt + kWsQcntBytes;
+    w.amax = w.lgcnt + kWsLgcntBytes;
+    size_t o = kWsWords;
     w.gact = o;   o += 256;
     w.codes = o;  o += up256((size_t)M * C / 2);
     w.scales = o; o += up256((size_t)M * C / 16);

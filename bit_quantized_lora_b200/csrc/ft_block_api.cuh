@@ -58,6 +58,9 @@ size_t norm_bwd_partials(int64_t M, int64_t D, int64_t B) {
     const int64_t chunk = std::min(norm_bwd_chunk(M, D, false), norm_bwd_chunk(M, D, true));
     return (size_t)((M + chunk - 1) / chunk + B) * 3 * (size_t)D;
 }
+// The sums that a backward leaves in a workspace: behind the linears' words,
+// which an FP32 sum over them would break for every later call of theirs.
+float* ws_sums(void* ws) { return ws ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kWsWords) : nullptr; }
 
 ft_status check_norm(const ft_gated_norm* n) {
     if (!n || n->M < 0 || n->D < 0 || n->B < 1) return FT_ERR_INVALID_ARG;
@@ -334,7 +337,7 @@ extern "C" {
 
 size_t ft_gated_norm_workspace_bytes(int64_t M, int64_t D, int64_t B) {
     if (M < 0 || M > kMaxRows || D < 8 || D % 8 || D > kNormMaxD || B < 1 || B > kMaxRows) return 0;
-    return (norm_bwd_partials(M, D, B) + (size_t)B * 3 * (size_t)D) * sizeof(float);
+    return kWsWords + (norm_bwd_partials(M, D, B) + (size_t)B * 3 * (size_t)D) * sizeof(float);
 }
 
 ft_status ft_gated_norm_fwd(const ft_gated_norm* n, const void* x, int64_t ldx, const void* y, int64_t ldy, void* r,
@@ -464,7 +467,7 @@ ft_status ft_gated_norm_bwd(const ft_gated_norm* n, const void* dh, int64_t lddh
         p.dy = static_cast<__nv_bfloat16*>(g->dy);
         p.lddy = g->lddy;
         p.amax = g->amax_dy;
-        p.partial = static_cast<float*>(ws);
+        p.partial = ws_sums(ws);
         p.need_s = need_s;
         p.need_t = need_t;
         p.has = norm_has(n) | (dh ? ft::norm::kDh : 0u) | (dr ? ft::norm::kDr : 0u) | (p.r ? ft::norm::kR : 0u) |
@@ -496,7 +499,7 @@ ft_status ft_gated_norm_bwd(const ft_gated_norm* n, const void* dh, int64_t lddh
     q.w_post = n->w_post;
     q.w = n->w;
     q.bias = n->bias;
-    q.partial = static_cast<const float*>(ws);
+    q.partial = ws_sums(ws);
     q.dgate = g->dgate;
     q.dscale = g->dscale;
     q.dshift = g->dshift;
@@ -505,7 +508,7 @@ ft_status ft_gated_norm_bwd(const ft_gated_norm* n, const void* dh, int64_t lddh
     q.dbias = g->dbias;
     q.need_s = need_s;
     q.need_t = need_t;
-    if (g->dw_post || g->dw || g->dbias) q.sums = static_cast<float*>(ws) + norm_bwd_partials(n->M, n->D, n->B);
+    if (g->dw_post || g->dw || g->dbias) q.sums = ws_sums(ws) + norm_bwd_partials(n->M, n->D, n->B);
     LaunchTimer lt(KID_NORM_REDUCE, st);
     // partial rows of a sample of average length
     const bool few = n->M / chunk / n->B < 8;
@@ -566,7 +569,7 @@ ft_status ft_qk_rope_fwd(const ft_rope* R, const void* qkv, int64_t ld, const ft
 
 size_t ft_qk_rope_workspace_bytes(int64_t M, int64_t hd) {
     if (M < 0 || hd < 0) return 0;
-    return (size_t)kRopeMaxBlocks * 2 * (size_t)hd * sizeof(float);
+    return kWsWords + (size_t)kRopeMaxBlocks * 2 * (size_t)hd * sizeof(float);
 }
 
 ft_status ft_qk_rope_bwd(const ft_rope* R, const ft_heads* dq, const ft_heads* dk, const ft_heads* dv,
@@ -597,7 +600,7 @@ ft_status ft_qk_rope_bwd(const ft_rope* R, const ft_heads* dq, const ft_heads* d
         p.dx = static_cast<__nv_bfloat16*>(dqkv);
         p.lddx = lddqkv;
         p.amax = amax;
-        p.partial = dw ? static_cast<float*>(ws) : nullptr;
+        p.partial = dw ? ws_sums(ws) : nullptr;
         blocks = rope_grid<true>(&p);
         LaunchTimer lt(KID_ROPE_BWD, st);
         const ft_status e = launch_rope<true>(p, blocks, d, st);
@@ -607,7 +610,7 @@ ft_status ft_qk_rope_bwd(const ft_rope* R, const ft_heads* dq, const ft_heads* d
     if (!dw) return FT_OK;
     LaunchTimer lt(KID_ROPE_REDUCE, st);
     const ft_status e = launch_overlapped_args(ft::rope::k_qk_rope_reduce, 2 * R->hd / 8, 1024, 0, st,
-                                               static_cast<const float*>(ws), blocks, (int)R->hd, dw_q, dw_k);
+                                               static_cast<const float*>(ws_sums(ws)), blocks, (int)R->hd, dw_q, dw_k);
     lt.stop();
     return e;
 }

@@ -397,7 +397,9 @@ size_t ft_linear_fwd_noalloc_max_bytes(void);
  *   - They keep no state between calls and use no epochs: a call may be
  *     captured in a CUDA graph and replayed.  A workspace serves one call at
  *     a time (calls that may run at the same time take one each, graphs
- *     among them); it needs no clearing.
+ *     among them); it needs no clearing.  It may be the linears' workspace,
+ *     used in turn: these calls leave the words alone that those keep in it
+ *     (which is why their workspace sizes are not those of the sums alone).
  *   - An output may be the very buffer of an input of the same type, shape
  *     and leading dimension (in place); buffers that overlap otherwise are
  *     outside the contract.
