@@ -45,6 +45,7 @@ struct DevInfo {
     // of launches with dynamic shared memory, by kernel, threads and bytes:
     // blocks that an SM holds (asking takes longer than the launch)
     std::map<std::tuple<const void*, int, size_t>, int> per_sm;
+    std::map<const void*, size_t> smem_allowed;  // by kernel: what its launches may take
 };
 DevInfo g_dev[64];
 std::mutex g_mu;
@@ -90,6 +91,7 @@ ft_status device_info(DevInfo** out) {
     if (d.attr_set && d.ctx != ctx) {  // a new context: set the attributes again
         d.attr_set = false;
         d.per_sm.clear();
+        d.smem_allowed.clear();
     }
     if (!d.init) {
         int major = 0, minor = 0, sms = 0;

@@ -94,15 +94,21 @@ uint32_t norm_has(const ft_gated_norm* n) {
            (n->post == FT_NORM_LAYER ? kPostMean : 0u);
 }
 // Blocks of `k` that an SM holds; lets the kernel take its shared memory
-// first.  Asked once per kernel and launch shape in a context.
+// first.  Asked once per kernel and launch shape in a context.  The limit is
+// the kernel's, and one kernel serves many widths: it is only ever raised, so
+// that a shape asked for before (or by another thread meanwhile) still fits.
 ft_status blocks_per_sm(const void* k, int threads, size_t smem, DevInfo* d, int* out) {
     try {
         std::lock_guard<std::mutex> lk(g_mu);
         int& n = d->per_sm[std::make_tuple(k, threads, smem)];
         if (n == 0) {
             int got = 0;
-            if (smem > 32 * 1024)  // with the static part, above what a launch may take unasked
+            size_t& allowed = d->smem_allowed[k];
+            // 32 KB and the static part are less than a launch may take unasked
+            if (smem > std::max<size_t>(allowed, 32 * 1024)) {
                 FT_TRY(cuda_ok(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)));
+                allowed = smem;
+            }
             FT_TRY(cuda_ok(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&got, k, threads, smem)));
             n = std::max(1, got);
         }
