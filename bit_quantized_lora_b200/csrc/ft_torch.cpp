@@ -1,6 +1,7 @@
 // ft_torch.cpp -- the torch side of the operators around the linears: checks
 // of tensors, allocation of the outputs that a call was not given, and the
-// calls of the C ABI (include/ft.h).  Marshalling only, in C++ because a small
+// calls of the C ABI (include/ft.h); for the optimizer, the look at its
+// tensors before a step.  Marshalling only, in C++ because a small
 // call's host time is what its user waits for: the same checks took 15 to 45
 // us per call in Python, more than the kernels.  The Python functions
 // (blockops.py) document the arguments, and put the tensors' device and stream
@@ -385,6 +386,24 @@ py::tuple qk_rope_bwd(const py::object& rope, const Tensor& dq, const Tensor& dk
     return py::make_tuple(dqkv, dw_q, dw_k);
 }
 
+// ---------------------------------------------------------------- optimizer
+// What a step takes for granted of its tensors, as bytes to compare with those
+// of the step before: where each lies, its type, sizes and strides.
+py::bytes layout_of(const py::sequence& tensors) {
+    std::string key;
+    key.reserve(64 * py::len(tensors));
+    auto put = [&](int64_t v) { key.append(reinterpret_cast<const char*>(&v), sizeof(v)); };
+    for (const py::handle& h : tensors) {
+        if (!THPVariable_Check(h.ptr())) type_error("parameters and gradients must be tensors");
+        const Tensor& t = THPVariable_Unpack(h.ptr());
+        put(reinterpret_cast<int64_t>(t.data_ptr()));
+        put((int64_t)t.scalar_type() << 32 | t.dim());
+        for (int64_t n : t.sizes()) put(n);
+        for (int64_t n : t.strides()) put(n);
+    }
+    return py::bytes(key);
+}
+
 }  // namespace
 
 PYBIND11_MODULE(_ft_torch, m) {
@@ -393,4 +412,5 @@ PYBIND11_MODULE(_ft_torch, m) {
     m.def("gelu_bwd", &gelu_bwd);
     m.def("qk_rope_fwd", &qk_rope_fwd);
     m.def("qk_rope_bwd", &qk_rope_bwd);
+    m.def("layout_of", &layout_of);
 }

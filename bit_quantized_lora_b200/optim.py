@@ -13,7 +13,7 @@ import struct
 import numpy as np
 import torch
 
-from ._lib import FtAdamwTensor, check, load
+from ._lib import FtAdamwTensor, check, load, load_torch
 from .blockops import _on_device
 
 _DTYPE = {torch.bfloat16: 0, torch.float32: 1}
@@ -118,7 +118,8 @@ class AdamW:
                     self.master[s * BLOCK:s * BLOCK + p.numel()].copy_(p.detach().reshape(-1))
         self._step = torch.zeros(2, dtype=torch.int64, device=dev)
         self.step_count = self._step[:1]
-        # the tensors' records; a step looks whether a caller has exchanged memory and writes the new addresses
+        # the tensors' records; a step looks whether a caller has exchanged one (its memory, type, sizes or strides),
+        # checks it as at first and writes the new addresses
         self._starts = starts.astype(np.uint64) * np.uint64(BLOCK)
         self._has_master = np.array(has_master)
         self._is16 = np.array([p.dtype == torch.bfloat16 for p in self.params])
@@ -127,7 +128,7 @@ class AdamW:
         self._rec["weight_decay"] = decay
         self._rec_addr = self._rec.ctypes.data
         self._bind()
-        self._bind_params(self._memory(self.params))
+        self._bind_params(load_torch().layout_of(self.params))
         self._lent, self._seen_grads = True, None  # the records hold no gradients of the optimizer's own yet
         self.grads = None if grads is None else self._checked(grads)
 
@@ -143,32 +144,29 @@ class AdamW:
         self._rec["gt"] = [_DTYPE[g.dtype] for g in grads]
         return grads
 
-    @staticmethod
-    def _memory(ts) -> list:
-        return [(t.data_ptr(), t.nbytes) for t in ts]
-
     def step(self, grads=None, lr=None, grad_scale: torch.Tensor | None = None, stream=None) -> None:
         """One step from `grads` (or the optimizer's own).  lr: a float, or a
         float32 device scalar (a captured step whose rate changes), in place
         of the optimizer's.  grad_scale: a float32 device scalar that
         multiplies the gradients (1 / ranks, a clipping factor)."""
+        layout = load_torch().layout_of
         if grads is not None:
             self._lend(grads)
         elif self.grads is None:
             raise ValueError("step() needs gradients")
         else:
-            memory = self._memory(self.grads)
-            if self._lent or memory != self._seen_grads:  # the last step read others, or a caller exchanged one
+            seen = layout(self.grads)
+            if self._lent or seen != self._seen_grads:  # the last step read others, or a caller exchanged one
                 self._lend(self.grads)
-                self._seen_grads, self._lent = memory, False
+                self._seen_grads, self._lent = seen, False
         held = self._held
         if not (held[0] is self.master and held[1] is self.exp_avg and held[2] is self.exp_avg_sq and
                 held[3] is self.exp_avg_scale and held[4] is self.exp_avg_sq_scale):
             raise ValueError("the state's tensors are the optimizer's own: load_state_dict() exchanges their values")
-        memory = self._memory(self.params)
-        if memory != self._seen:  # a caller has given a parameter other memory
+        seen = layout(self.params)
+        if seen != self._seen:  # a caller has given a parameter other memory, or another view of its own
             _check_params(self.params, self._step.device, self._dtypes, self._sizes)
-            self._bind_params(memory)
+            self._bind_params(seen)
         self._launch(self._step, self.lr if lr is None else lr, grad_scale, stream=stream)
 
     def _lend(self, grads) -> None:
@@ -176,12 +174,12 @@ class AdamW:
         self._lent = True
         self._rec["grad"] = [t.data_ptr() for t in self._checked(grads)]
 
-    def _bind_params(self, memory) -> None:
-        """The parameters' addresses in the tensors' records."""
-        rec, own = self._rec, np.array([a for a, _ in memory], np.uint64)
+    def _bind_params(self, seen: bytes) -> None:
+        """The parameters' addresses in the tensors' records; seen: their layout."""
+        rec, own = self._rec, np.array([p.data_ptr() for p in self.params], np.uint64)
         rec["p16"] = np.where(self._is16, own, 0)
         rec["p"] = np.where(self._has_master, self._master_ptrs, np.where(self._is16, 0, own))
-        self._seen = memory
+        self._seen = seen
 
     def _bind(self) -> None:
         """The state's addresses in the tensors' records."""

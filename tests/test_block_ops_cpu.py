@@ -341,3 +341,20 @@ def test_calls_by_position_and_by_name_refuse_alike():
                  lambda: ft.ft_adamw_decode(x, x), lambda: ft.ft_adamw_decode(codes=x, scales=x)):
         with pytest.raises(TypeError, match="CUDA"):
             call()
+
+
+def test_the_layout_of_an_optimizers_tensors():
+    """What a step compares with the step before: memory, type, sizes and
+    strides of every tensor, in order."""
+    layout = _lib.load_torch().layout_of
+    a, b = torch.zeros(16, 16), torch.zeros(64, dtype=torch.bfloat16)
+    key = layout([a, b])
+    assert key == layout((a, b)) == layout([a.view(16, 16), b.detach()])
+    for other in ([b, a], [a], [a.t(), b], [a.view(8, 32), b], [a.clone(), b], [a[:8], b], [a.view(torch.int32), b],
+                  [a, b.view(torch.float16)], [a, b.view(torch.int8)], [a, b[1:]], [a, b[::2]], [a, b, b], []):
+        assert layout(other) != key
+    assert layout([]) == layout(())
+    assert layout([torch.zeros(0)]) == layout([torch.zeros(0)]) != layout([torch.zeros(0, dtype=torch.int32)])
+    for bad in ([None], [a, 3]):
+        with pytest.raises(TypeError):
+            layout(bad)

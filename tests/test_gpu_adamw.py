@@ -405,3 +405,28 @@ def test_a_refused_step_on_lent_gradients_leaves_no_trace():
     opt.step(others), ref.step(iter(others))
     opt.step(), ref.step()
     assert all(torch.equal(a, b) for a, b in zip(params, twin)) and int(opt.step_count) == 4
+
+
+def test_memory_seen_another_way_is_looked_at_too():
+    """The same bytes under other strides or as another type: refused like
+    other memory, before anything is stepped; the old view steps on."""
+    for gdt in (F32, BF16):
+        params, grads = make([256, 64], pdt=gdt, gdt=gdt, seed=21)
+        params, grads = [p.view(-1, 8) for p in params], [g.view(-1, 8) for g in grads]
+        params[0], grads[0] = params[0].view(16, 16), grads[0].view(16, 16)
+        twin = [p.clone() for p in params]
+        opt, ref = ft.AdamW(params, grads, master=False), ft.AdamW(twin, [g.clone() for g in grads], master=False)
+        opt.step(), ref.step()
+        p, g = params[0].data, grads[0].data
+        other = torch.float16 if gdt == BF16 else BF16
+        for t, held, views in ((params[0], p, (p.t(), p.view(torch.int16), p.view(other))),
+                               (grads[0], g, (g.t(), g.view(torch.int16), g.view(other), g.view(8, 32)))):
+            for view in views:
+                assert view.data_ptr() == held.data_ptr() and view.nbytes == held.nbytes
+                t.data = view
+                with pytest.raises((ValueError, TypeError)):
+                    opt.step()
+                t.data = held
+        assert int(opt.step_count) == 1
+        opt.step(), ref.step()
+        assert all(torch.equal(a, b) for a, b in zip(params, twin)) and int(opt.step_count) == 2
