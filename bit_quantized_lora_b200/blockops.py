@@ -110,7 +110,9 @@ def ft_gated_norm_bwd(norm: GatedNorm, dh: torch.Tensor | None, r: torch.Tensor 
     param_grads: True for the gradient of every parameter given, or the names
     wanted out of 'gate', 'scale', 'shift', 'weight', 'bias', 'w_post'; a
     gate, scale or shift that all samples share gets the sum over them.
-    amax_dy: an optional float32 device scalar (>= 0) raised to max|dy|."""
+    amax_dy: an optional float32 device scalar (>= 0) raised to max|dy|.  ws:
+    a Workspace for the parameters' sums in place of scratch of the call's own
+    (it may be the linears', in turn)."""
     some = dh if dh is not None else dr
     if some is None:
         raise ValueError("one of dh and dr must be given")
@@ -194,5 +196,9 @@ def ft_qk_rope_bwd(rope: Rope, dq: torch.Tensor, dk: torch.Tensor, dv: torch.Ten
     head_dim], any strides).  qkv: the forward's input, needed with the norm
     (not after a forward in place).  dv=None leaves dqkv's value columns as
     they are (zero where dqkv is not given).  amax: an optional float32 device
-    scalar (>= 0) raised to max|dqkv|.  Returns (dqkv, dw_q, dw_k)."""
+    scalar (>= 0) raised to max|dqkv| over the columns written: with dv=None
+    it does not see a given dqkv's value columns, so raise it to max|dv| too
+    before ft_linear_bwd takes it.  ws: a Workspace for the weights' sums in
+    place of scratch of the call's own (it may be the linears', in turn).
+    Returns (dqkv, dw_q, dw_k)."""
     return load_torch().qk_rope_bwd(rope, dq, dk, dv, pos, qkv, dqkv, weight_grads, amax, ws)

@@ -249,3 +249,18 @@ def test_refusals():
     with pytest.raises(ft.FtError):  # head strides that are not multiples of eight
         q = torch.zeros(1, 4, 5, 68, dtype=BF16, device="cuda")[..., :64]
         ft.ft_qk_rope_fwd(c.rope, c.qkv, c.pos, q=q)
+
+
+def test_amax_without_the_gradient_of_v():
+    """Without dv the amax is that of the columns written: what lies in the
+    value columns, a gradient already there or not yet, does not count."""
+    c = Case(B=2, S=13, Hq=4, Hk=2, hd=64)
+    cut = 6 * 64
+    for fill in (100.0, float("nan")):
+        left = torch.full((c.M, c.width), fill, dtype=BF16, device="cuda")
+        amax = torch.zeros(1, device="cuda")
+        ft.ft_qk_rope_bwd(c.rope, c.d["q"], c.d["k"], None, c.pos, qkv=c.qkv, dqkv=left, amax=amax)
+        assert 0.0 < float(amax) == float(left[:, :cut].float().abs().max()) < 1.0
+    amax = torch.zeros(1, device="cuda")  # value columns that the call makes are zero: the amax is all of dqkv's
+    dqkv, _, _ = ft.ft_qk_rope_bwd(c.rope, c.d["q"], c.d["k"], None, c.pos, qkv=c.qkv, amax=amax)
+    assert float(amax) == float(dqkv.float().abs().max())
