@@ -264,3 +264,23 @@ def test_amax_without_the_gradient_of_v():
     amax = torch.zeros(1, device="cuda")  # value columns that the call makes are zero: the amax is all of dqkv's
     dqkv, _, _ = ft.ft_qk_rope_bwd(c.rope, c.d["q"], c.d["k"], None, c.pos, qkv=c.qkv, amax=amax)
     assert float(amax) == float(dqkv.float().abs().max())
+
+
+# Rows of the last round, more than half as many as the device holds warps (2960 backward with the norm, 4736
+# otherwise), cut into three slices of its turns of heads in one direction or both, with whole rows before them or not.
+SLICED = [
+    dict(S=2841, Hq=16, Hk=8, hd=32, axes=(8, 12, 12)),
+    dict(S=1700, Hq=16, Hk=8, hd=32, axes=(8, 12, 12)),
+    dict(S=4660, Hq=10, Hk=2, hd=40, axes=(16, 24), halves=True),
+    dict(S=2841, Hq=10, Hk=2, hd=40, axes=(16, 24), halves=True, norm=False),
+    dict(S=7577, Hq=7, Hk=7, hd=64, axes=(16, 24, 24), norm=False),
+    dict(S=4608, Hq=24, Hk=24, hd=128, axes=(16, 56, 56)),
+]
+
+
+@pytest.mark.parametrize("kw", SLICED, ids=lambda k: "-".join(f"{a}{v}" for a, v in k.items()))
+def test_rows_cut_into_slices(kw):
+    c = Case(seed=5, **kw)
+    c.check_forward(*ft.ft_qk_rope_fwd(c.rope, c.qkv, c.pos))
+    amax = torch.zeros(1, device="cuda")
+    c.check_backward(*ft.ft_qk_rope_bwd(c.rope, c.d["q"], c.d["k"], c.d["v"], c.pos, qkv=c.qkv, amax=amax), amax)
