@@ -434,3 +434,21 @@ def test_python_refusals():
         ft.ft_gated_norm_bwd(c.norm, c.dh, r, stats, gate=c.gate)
     with pytest.raises(ValueError):
         ft.ft_gated_norm_bwd(c.norm, c.dh, r, stats, param_grads=("bias",))
+
+
+@pytest.mark.parametrize("D,xt", [(1024, BF16), (264, F32), (4096, F32)], ids=str)
+def test_a_scale_next_to_minus_one(D, xt):
+    """1 + scale of a few 2^-24 (a channel that the modulation all but
+    closes): h is still (N(r)) (1 + scale) to its own rounding, not to that
+    of the scale."""
+    c = Case(6, D, xt=xt, seed=D)
+    k = torch.arange(D, device="cuda") % 5
+    c.scale = (k * 2.0 ** -24 - 1.0).view(1, D)
+    c.shift = torch.zeros(1, D, device="cuda")
+    assert c.scale.dtype == F32 and torch.equal(c.scale.double(), (k.double() * 2.0 ** -24 - 1.0).view(1, D))
+    r, h, _ = c.forward()
+    rs = r.double()
+    n, m, rstd = R.norm64(rs, c.pre, c.eps)
+    avg = rs.abs().mean(1, keepdim=True)
+    a = 1 + c.scale.double()
+    R.check_rounded(h, n * a, C * (rs.abs() + avg) * rstd * (1 + avg * rstd) * a)
