@@ -6,7 +6,8 @@ ft_linear_bwd quantize in a single pass.
 
 Calls run on `stream`, or on the current stream of their tensors' device;
 what they allocate (outputs that are not given, scratch) belongs to that
-stream.  They may be captured in a CUDA graph.
+stream.  They may be captured in a CUDA graph, which then owns their scratch
+(a Workspace that the call is given is not used in a capture).
 """
 from __future__ import annotations
 

@@ -6,6 +6,7 @@
 // us per call in Python, more than the kernels.  The Python functions
 // (blockops.py) document the arguments, and put the tensors' device and stream
 // in place first.
+#include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/extension.h>
 
@@ -70,9 +71,12 @@ int dtype_of(at::ScalarType t, const char* what) {
 }
 
 // Scratch of one call: the caller's workspace, or memory of the current
-// stream (an allocation that a captured graph owns with the call).
+// stream.  A captured call always takes the latter, which its graph owns: a
+// workspace gives its memory back when a later call needs more, and the graph
+// would go on writing there.
 Tensor scratch(const py::object& ws, size_t bytes, const Tensor& like) {
-    if (!ws.is_none()) return ws.attr("get")(bytes, py::cast(like).attr("device")).cast<Tensor>();
+    if (!ws.is_none() && c10::cuda::currentStreamCaptureStatusMayInitCtx() == c10::cuda::CaptureStatus::None)
+        return ws.attr("get")(bytes, py::cast(like).attr("device")).cast<Tensor>();
     return at::empty({(int64_t)bytes}, like.options().dtype(at::kByte));
 }
 

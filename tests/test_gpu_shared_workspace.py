@@ -16,19 +16,25 @@ def inputs(seed):
     return lambda *s, std=1.0: (torch.randn(*s, generator=g, device="cuda") * std).to(BF16)
 
 
-def operators(ws, seed=1):
-    """The two backward calls that keep sums in a workspace; all they return."""
+def made(seed=1):
+    """The two backward calls that keep sums in a workspace, as functions of
+    it."""
     rnd = inputs(seed)
     norm = ft.GatedNorm(pre=ft.NORM_LAYER, post=ft.NORM_RMS, weight=rnd(K), bias=rnd(K), w_post=rnd(K))
     x, y, dh, dr, mod = rnd(M, K), rnd(M, K), rnd(M, K), rnd(M, K), rnd(2, 3 * K)
     gate, scale, shift = mod[:, :K], mod[:, K:2 * K], mod[:, 2 * K:]
     r, h, stats = ft.ft_gated_norm_fwd(norm, x, y, gate, scale, shift)
-    d = ft.ft_gated_norm_bwd(norm, dh, r, stats, dr=dr, y=y, gate=gate, scale=scale, shift=shift, ws=ws)
     rope = ft.Rope(6, 3, 64, (32, 32), ft.rope_freqs((32, 32)), norm=True, w_q=rnd(64), w_k=rnd(64))
     pos = torch.arange(2 * M, device="cuda", dtype=torch.int32).view(M, 2)
     dq, dk, dv = (rnd(1, n, M, 64) for n in (6, 3, 3))
-    out = ft.ft_qk_rope_bwd(rope, dq, dk, dv, pos, qkv=rnd(M, rope.width), ws=ws)
-    return [d.dx, d.dy, d.dgate, d.dscale, d.dshift, d.dweight, d.dbias, d.dw_post, *out]
+    qkv = rnd(M, rope.width)
+
+    def run(ws):
+        d = ft.ft_gated_norm_bwd(norm, dh, r, stats, dr=dr, y=y, gate=gate, scale=scale, shift=shift, ws=ws)
+        out = ft.ft_qk_rope_bwd(rope, dq, dk, dv, pos, qkv=qkv, ws=ws)
+        return [d.dx, d.dy, d.dgate, d.dscale, d.dshift, d.dweight, d.dbias, d.dw_post, *out]
+
+    return run
 
 
 def linears(ws, layer, seed=2):
@@ -43,6 +49,7 @@ def test_the_words_are_left_alone():
     ws = ft.Workspace()
     buf = ws.get(1 << 24, torch.device("cuda", 0))
     buf.fill_(0xA5)
+    operators = made()
     want = operators(None)
     got = operators(ws)
     assert ws.buf is buf
@@ -58,6 +65,7 @@ def test_linears_and_operators_in_turn(rows, monkeypatch):
     rnd = inputs(0)
     layer = ft.prepare_layer(W_res=rnd(N, K, std=K ** -0.5), U=rnd(K, 16, std=0.1), V=rnd(N, 16, std=0.1),
                              A=rnd(K, 16, std=0.1), B=rnd(N, 16, std=0.1), s=0.5)
+    operators = made()
     want_l, want_o = linears(ft.Workspace(), layer), operators(ft.Workspace())
     x = inputs(3)(rows, K)
     want_q = ft.ft_quantize(x, ws=ft.Workspace())
@@ -72,3 +80,28 @@ def test_linears_and_operators_in_turn(rows, monkeypatch):
         assert all(torch.equal(a, b) for a, b in zip(operators(ws), want_o))
     torch.cuda.synchronize()
     assert ft.ft_device_error() == 0
+
+
+def test_a_captured_call_owns_its_scratch():
+    """A workspace may grow, and so give its memory back, while a graph that
+    was captured with it lives: the graph writes neither there nor to what
+    lies there afterwards."""
+    operators, ws = made(), ft.Workspace()
+    want = operators(None)
+    operators(ws)  # sized by a call outside the graph
+    size = ws.buf.numel()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = operators(ws)
+    ws.buf.fill_(0xA5)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, want)) and bool((ws.buf == 0xA5).all())
+    ws.get(8 * size, torch.device("cuda", 0))
+    others = [torch.full((size,), 7, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    for t in out:
+        t.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, want)) and not ws.buf.any()
+    assert all(bool((t == 7).all()) for t in others)
