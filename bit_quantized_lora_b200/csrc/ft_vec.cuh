@@ -35,23 +35,12 @@ __device__ __forceinline__ uint2 ld_stream_v2(const void* p) {
     asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
     return v;
 }
-__device__ __forceinline__ void load8(Raw8<__nv_bfloat16>& r, const __nv_bfloat16* p) { r.a = ld_stream_v4(p); }
-__device__ __forceinline__ void load8(Raw8<float>& r, const float* p) {
-    r.a = ld_stream_v4(p);
-    r.b = ld_stream_v4(p + 4);
-}
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
     f[0] = bf16_lo(v.x), f[1] = bf16_hi(v.x), f[2] = bf16_lo(v.y), f[3] = bf16_hi(v.y);
     f[4] = bf16_lo(v.z), f[5] = bf16_hi(v.z), f[6] = bf16_lo(v.w), f[7] = bf16_hi(v.w);
-}
-__device__ __forceinline__ void unpack8(const Raw8<__nv_bfloat16>& r, float (&f)[8]) { unpack8(r.a, f); }
-__device__ __forceinline__ void unpack8(const Raw8<float>& r, float (&f)[8]) {
-    f[0] = __uint_as_float(r.a.x), f[1] = __uint_as_float(r.a.y), f[2] = __uint_as_float(r.a.z);
-    f[3] = __uint_as_float(r.a.w), f[4] = __uint_as_float(r.b.x), f[5] = __uint_as_float(r.b.y);
-    f[6] = __uint_as_float(r.b.z), f[7] = __uint_as_float(r.b.w);
 }
 
 // Asynchronous 16-byte copies into a thread's own shared-memory slots: what a
@@ -147,23 +136,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
     return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
 }
-// Stores eight values rounded to T and leaves them in f as stored.
-__device__ __forceinline__ void store8(__nv_bfloat16* p, float (&f)[8]) {
-    const uint4 v = pack8(f);
-    *reinterpret_cast<uint4*>(p) = v;
-    unpack8(v, f);
-}
-__device__ __forceinline__ void store8(float* p, float (&f)[8]) {
-    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
-}
-
-// Rounds eight values to T as they would be loaded again.
-__device__ __forceinline__ void round8(Raw8<__nv_bfloat16>& r, const float (&f)[8]) { r.a = pack8(f); }
-__device__ __forceinline__ void round8(Raw8<float>& r, const float (&f)[8]) {
-    r.a = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-    r.b = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
-}
 __device__ __forceinline__ void put8(__nv_bfloat16* p, const Raw8<__nv_bfloat16>& r) {
     *reinterpret_cast<uint4*>(p) = r.a;
 }
@@ -171,6 +143,7 @@ __device__ __forceinline__ void put8(float* p, const Raw8<float>& r) {
     *reinterpret_cast<uint4*>(p) = r.a;
     *reinterpret_cast<uint4*>(p + 4) = r.b;
 }
+// Rounds eight values to T as they would be loaded again.
 __device__ __forceinline__ void round8(Raw8<__nv_bfloat16>& r, const F8& f) {
     r.a = make_uint4(pack_bf16(f.p[0].x, f.p[0].y), pack_bf16(f.p[1].x, f.p[1].y), pack_bf16(f.p[2].x, f.p[2].y),
                      pack_bf16(f.p[3].x, f.p[3].y));
@@ -206,15 +179,6 @@ __device__ __forceinline__ uint32_t store8_max(__nv_bfloat16* p, const float (&f
 }
 
 // Eight values of a parameter vector (bf16 or FP32, 16-byte aligned), cached.
-__device__ __forceinline__ void load_param8(const void* p, int64_t i, bool f32, float (&f)[8]) {
-    if (f32) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + i));
-        const float4 b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + i + 4));
-        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-    } else {
-        unpack8(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i)), f);
-    }
-}
 template <bool k32>
 __device__ __forceinline__ F8 load_param8(const void* p, int64_t i) {
     if constexpr (k32) {
@@ -229,12 +193,6 @@ __device__ __forceinline__ F8 load_param8(const void* p, int64_t i) {
 __device__ __forceinline__ float load_param(const void* p, int64_t i, bool f32) {
     return f32 ? __ldg(static_cast<const float*>(p) + i)
                : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-}
-
-__device__ __forceinline__ float max_abs8(const float (&f)[8], float m) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[i]));
-    return m;
 }
 
 // Raises *out to the block's largest m (all threads of the block call it;
