@@ -10,10 +10,11 @@ returns through a gate,
     h2 = N(r) (1 + scale2) + shift2        x' = r + gate2 Down(GELU(Up(h2)))
 
 `DitBlock` runs its forward and its backward over the C ABI: the residual of
-one half and the norm of the next are one kernel, and every kernel that
-writes a linear's input (or output gradient) finds its tensor amax on the
-way, so that the linear quantizes it in a single pass.  The attention itself
-is the caller's.
+one half and the norm of the next are one kernel.  The norms find the tensor
+amax of QKV's and Up's inputs on the way, and the kernel before each linear's
+backward that of its output gradient, so that these are quantized in a single
+pass; Out and Down look for their inputs' themselves (they follow the
+attention and GELU).  The attention itself is the caller's.
 """
 from __future__ import annotations
 

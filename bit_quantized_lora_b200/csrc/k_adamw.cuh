@@ -293,8 +293,13 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) k_adamw(const __grid_cons
                 g[i] = mul2(g[i], both(gs));
                 m[i] = sum_of(mul2(m[i], both(p.b1)), mul2(g[i], both(p.c1)));
                 v[i] = sum_of(mul2(v[i], both(p.b2)), mul2(mul2(g[i], both(p.c2)), g[i]));
-                // a few ulp of the step itself are far below the weight's;
-                // a subnormal v counts as zero next to eps
+                // hardware root and reciprocal, 2^-23 each: a few 2^-23 of the
+                // step, below the weight's own rounding unless the weight is
+                // small next to its step (a factor that starts at zero).  IEEE
+                // root and division took 138.6 instead of 135.7 us for the
+                // stack above with its decodings, 95.5 instead of 82.6 for
+                // bf16 weights without master, 6.2 instead of 5.4 for two small
+                // tensors.  A subnormal v counts as zero next to eps
                 float2 u = mul2(m[i], recip_near(fma2(sqrt_near(v[i]), both(rc2), both(p.eps))));
                 if (p.exact)
                     u = make_float2(m[i].x / fmaf(sqrtf(v[i].x), rc2, p.eps), m[i].y / fmaf(sqrtf(v[i].y), rc2, p.eps));

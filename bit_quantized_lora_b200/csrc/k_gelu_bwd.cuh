@@ -25,7 +25,8 @@ constexpr int kTab = 4096;
 constexpr int kU = 2;  // vectors of eight in flight per thread, of y and of dh
 
 // GELU'(y).  From |y| = 16 on the slope is 1 or 0 to more than FP32 shows
-// (y phi(y) < 2^-180 there, and its product with any bf16 underflows).
+// (y phi(y) < 2^-180 there, below the smallest subnormal); at the infinities
+// these are its limits.
 __device__ __forceinline__ float slope(float y) {
     if (fabsf(y) >= 16.0f) return y > 0.0f ? 1.0f : 0.0f;
     const float phi = __fmul_rn(0.39894228040143268f, expf(-0.5f * y * y));

@@ -19,15 +19,14 @@
 // taken about the mean (no cancellation), and the next rows' loads are in
 // flight while a row is reduced.  HBM bounds both kernels for many rows, 8 B
 // per element forward (x, y, r, h in bf16), 12 B backward (dh, dr, r, y, dx,
-// dy): of 1000 more rows of 3072 channels each costs 4.0 us and 5.7 us, 95 and
-// 99 % of the measured 6.53 TB/s.  At 4608 rows (30 us forward and 44 us
-// backward with its sums, replayed back to back, against 17.4 and 26.0) what
-// bounds them is the start, the drain and the instructions of a row, 27 and 47
-// per element: hence a
-// thread holds four vectors forward (fewer barriers and addresses per element;
-// one vector per thread took 41 us), sums come off in two-lane arithmetic, and
-// the usual modulated boundary is compiled apart (kMod: 29 us against 39 us
-// forward, 50 against 61 backward).  Backward a thread holds one vector up to
+// dy): from 4736 to 18944 rows of 3072 channels, 1000 more cost 4.0 us and 5.8
+// us, 93 and 98 % of the measured 6.53 TB/s.  At 4608 rows (30 us forward and
+// 44 us backward with its sums, replayed back to back, against 17.4 and 26.0)
+// what bounds them is the start, the drain and the instructions of a row, 27
+// and 47 per element: hence a thread holds four vectors forward (fewer barriers
+// and addresses per element; one vector per thread took 41 us), sums come off
+// in two-lane arithmetic, and the usual modulated boundary is compiled apart
+// (kMod: 30 us against 38 us forward, 44 against 55 backward).  Backward a thread holds one vector up to
 // 4096 channels, 80 registers and two blocks of 384 threads per SM at 3072
 // (two vectors and three blocks of 192: 45 against 44 us).
 #pragma once

@@ -490,6 +490,7 @@ size_t ft_gated_norm_workspace_bytes(int64_t M, int64_t D, int64_t B);
 /* ft_gelu_bwd_bf16 -- dy = dh * GELU'(y), GELU'(y) = Phi(y) + y phi(y): the
  * backward of ft_gelu_bf16, for the MLP's own backward.
  *   y, dh, dy: bf16 [n], 16-byte aligned; n a multiple of 8; dy may be dh or y.
+ *   At y = +Inf and -Inf GELU' is its limit, 1 and 0 (y phi(y) would be NaN).
  *   amax_dy: NULL, or a device float >= 0 raised to max|dy|.               */
 ft_status ft_gelu_bwd_bf16(const void* y, const void* dh, void* dy, int64_t n, float* amax_dy, void* stream);
 
@@ -583,7 +584,8 @@ typedef struct {
  * t = *step + 1:
  *     m = beta1 m + (1 - beta1) g        v = beta2 v + (1 - beta2) g^2
  *     p = p (1 - lr wd) - lr / (1 - beta1^t) * m / (sqrt(v / (1 - beta2^t)) + eps)
- * with g = grad * (*grad_scale).  The moments of the update are the fresh
+ * with g = grad * (*grad_scale).  The subtracted step is FP32 with a hardware
+ * root and reciprocal: good to a few 2^-23 of itself.  The moments of the update are the fresh
  * FP32 ones; with 8-bit states they are then stored as codes, per block of
  * 256 with top = the block's largest |m| (v), each step rounded to nearest
  * in IEEE FP32:
